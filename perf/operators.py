@@ -6,7 +6,7 @@ Three kinds of call, in the order a serving step makes them:
 * ``append``  new tokens' key rows go to their places in the pages, the position rotation applied on the way, and
   the same tokens' queries are rotated (latent cache in bf16 or E4M3, or keys and values of grouped kv heads);
 * ``window``  every query token attends to the keys of its sequence at positions up to its own, within the window
-  or among the first tokens (window 0: all of them), read through a block table;
+  or among the first tokens (window 0: all of them), read through a block table (the same three caches);
 * ``prefix``  all sequences of the batch attend to one shared prefix and each to its own further keys.
 
 ``run`` computes them with elementary torch operations in 32 bits where ``own`` is false and makes the calls of
@@ -45,8 +45,8 @@ def listed():
         # long chats, a window of 4096 and 4 first tokens
         {"name": "window, 64 long sequences", "op": "window", "kind": "mla", "B": 64, "Sq": 1, "H": 128, "Hkv": 1,
          "L_lo": 1000, "L_hi": 32768, "page": 64, "window": 4096, "first": 4, "sinks": False},
-        # two query tokens a sequence (a drafted one), few heads a GPU
-        {"name": "window, two tokens, 16 heads", "op": "window", "kind": "mla", "B": 132, "Sq": 2, "H": 16, "Hkv": 1,
+        # E4M3 pages, two query tokens a sequence (a drafted one), few heads a GPU
+        {"name": "window, E4M3, two tokens", "op": "window", "kind": "mla_fp8", "B": 132, "Sq": 2, "H": 16, "Hkv": 1,
          "L_lo": 1, "L_hi": 8192, "page": 64, "window": 2048, "first": 16, "sinks": True},
         # grouped kv heads with sink logits
         {"name": "window, grouped heads", "op": "window", "kind": "mha", "B": 64, "Sq": 1, "H": 32, "Hkv": 8,
@@ -81,8 +81,8 @@ def draw(rng):
         return {"op": op, "kind": kind, "B": B, "new": max(1, tokens // B), "spread": rng.choice([1, 10]), "H": H,
                 "Hkv": Hkv, "past": _spread(rng, 1, 2000), "page": page, "interleaved": rng.random() < 0.5}
     if op == "window":
-        kind = rng.choice(["mla", "mla", "mha"])
-        if kind == "mla":
+        kind = rng.choice(["mla", "mla", "mla_fp8", "mha"])
+        if kind != "mha":
             H, Hkv, Sq = rng.choice([16, 32, 64, 128]), 1, rng.choice([1, 1, 2, 3])
         else:
             (H, Hkv), Sq = rng.choice([(8, 8), (16, 2), (32, 8), (24, 3)]), rng.choice([1, 1, 2])
@@ -103,7 +103,8 @@ def _plan_lengths(case):
     """Lengths are part of the case: the same for every seed.  (lengths, new tokens of each sequence)"""
     rng = random.Random(repr(sorted((k, v) for k, v in case.items() if k != "name")))
     if case["op"] != "append":
-        return [rng.randint(case["L_lo"], case["L_hi"]) for _ in range(case["B"])], [case["Sq"]] * case["B"]
+        lengths = [rng.randint(case["L_lo"], case["L_hi"]) for _ in range(case["B"] - 1)]
+        return [case["L_hi"], *lengths], [case["Sq"]] * case["B"]  # one sequence is as long as the plan allows
     new = [max(1, _spread(rng, max(1, case["new"] // case["spread"]), case["new"])) for _ in range(case["B"])]
     return [rng.randint(0, case["past"]) + n for n in new], new
 
@@ -171,6 +172,8 @@ def prepare(case, seed):
         s["prefix_len"] = torch.tensor([case["P"]], dtype=torch.int32, device="cuda")
         pages += at
     s.update(cache(pages))
+    if case["kind"] == "mla_fp8":
+        s["kv_scale"] = float(torch.tensor(1.0 / 60.0, dtype=torch.float32))
     s["q"] = normal(B, Sq, H, D)
     s["scale"] = float(torch.tensor(D ** -0.5, dtype=torch.float32))
     s["sinks"] = normal(H, dtype=torch.float32) if case["sinks"] else None
@@ -185,8 +188,8 @@ def prepare(case, seed):
             s["plan"] = M.mha_decode_plan_paged(B, Sq, H, Hkv, L_max, page, window=case["window"],
                                                 first_tokens=case["first"])
         else:
-            s["plan"] = M.mla_decode_plan_paged(B, Sq, H, L_max, page, window=case["window"],
-                                                first_tokens=case["first"])
+            make = M.mla_decode_plan_paged_fp8 if case["kind"] == "mla_fp8" else M.mla_decode_plan_paged
+            s["plan"] = make(B, Sq, H, L_max, page, window=case["window"], first_tokens=case["first"])
         s["workspace"] = M.alloc_workspace(s["plan"])
     return s
 
@@ -219,6 +222,9 @@ def _run_own(s):
     elif case["kind"] == "mha":
         M.mha_decode_run_paged(s["plan"], s["q"], s["k_pages"], s["v_pages"], s["table"], s["seqlens"], s["scale"],
                                s["out"], s["lse"], s["workspace"], sinks=s["sinks"])
+    elif case["kind"] == "mla_fp8":
+        M.mla_decode_run_paged_fp8(s["plan"], s["q"], s["kv_pages"], s["kv_scale"], s["table"], s["seqlens"], s["scale"],
+                                   s["out"], s["lse"], s["workspace"], sinks=s["sinks"])
     else:
         M.mla_decode_run_paged(s["plan"], s["q"], s["kv_pages"], s["table"], s["seqlens"], s["scale"], s["out"],
                                s["lse"], s["workspace"], sinks=s["sinks"])
@@ -280,7 +286,11 @@ def _sequence_rows(s, pos):
     if case["kind"] == "mha":
         return (s["k_pages"].flatten(0, 1)[place].transpose(1, 2).float(),
                 s["v_pages"].flatten(0, 1)[place].transpose(1, 2).float())
-    kv = s["kv_pages"].flatten(0, 1)[place].float()[:, None]
+    if case["kind"] == "mla_fp8":
+        codes = s["kv_pages"].view(torch.uint8).flatten(0, 1)[place]
+        kv = (codes.view(torch.float8_e4m3fn).float() * s["kv_scale"])[:, None]
+    else:
+        kv = s["kv_pages"].flatten(0, 1)[place].float()[:, None]
     return kv, kv[..., :D_V]
 
 
@@ -382,7 +392,8 @@ def work(case):
         keys += case["P"]
         pairs += B * Sq * case["P"]
     rows, pages = B * Sq * H, keys // case["page"] + B
-    key, value = (Hkv * D_HEAD * 4, D_HEAD) if case["kind"] == "mha" else (D_QK * 2, D_V)
+    key, value = ((Hkv * D_HEAD * 4, D_HEAD) if case["kind"] == "mha" else
+                  (D_QK if case["kind"] == "mla_fp8" else D_QK * 2, D_V))
     width = D_HEAD if case["kind"] == "mha" else D_QK
     return {"bytes": keys * key + rows * (2 * width + 2 * value + 4) + 4 * pages + 4 * B,
             "flops": pairs * H * 2 * (width + value)}
@@ -432,12 +443,18 @@ def exact(case, seed):
     lses = torch.empty(B, Sq, H, dtype=torch.float64, device="cuda")
     keys = [s[n].flatten(0, 1) for n in (("k_pages", "v_pages") if case["kind"] == "mha" else ("kv_pages", "kv_pages"))]
     at = [e * page + r for e in s["prefix_table"].tolist() for r in range(page)][:case["P"]] if "P" in case else []
-    shared = keys[0][torch.tensor(at, dtype=torch.long, device="cuda")].double()
+    shared = None if case["op"] != "prefix" else keys[0][torch.tensor(at, dtype=torch.long, device="cuda")].double()
     for b, L in enumerate(lengths):
         rows = [table[b][p // page] * page + p % page for p in range(L)]
         rows = torch.tensor(rows, dtype=torch.long, device="cuda")
-        k, v = (x[rows].double() for x in keys)
-        k, v = (k, v) if case["kind"] == "mha" else (torch.cat([shared, k])[:, None], torch.cat([shared, v])[:, None, :D_V])
+        if case["kind"] == "mla_fp8":
+            k = v = keys[0].view(torch.uint8)[rows].view(torch.float8_e4m3fn).double() * s["kv_scale"]
+        else:
+            k, v = (x[rows].double() for x in keys)
+        if case["kind"] != "mha":
+            k, v = k[:, None], v[:, None, :D_V]
+            if case["op"] == "prefix":
+                k, v = torch.cat([shared[:, None], k]), torch.cat([shared[:, None, :D_V], v])
         for t in range(Sq):
             p, w = L - Sq + t, case.get("window", 0)
             sees = set(range(max(0, p + 1 - w) if w else 0, p + 1)) | set(range(min(case.get("first", 0), p + 1)))
