@@ -55,7 +55,10 @@ typedef enum mla_status {
     MLA_ERR_CUDA = 4,          /* a CUDA runtime / driver call failed (launch, attribute, ...) */
     MLA_ERR_TIMEOUT = 5,       /* device: a bounded pipeline wait ran out; results are invalid */
     MLA_ERR_WORKSPACE = 6,     /* workspace pointer null or smaller than the plan requires */
-    MLA_ERR_SEQLEN = 7         /* device: some seqlens[b] was < 0 or > L_max (clamped to [0, L_max]) */
+    MLA_ERR_SEQLEN = 7,        /* device: some seqlens[b] was < 0 or > L_max (clamped to [0, L_max]), or an
+                                  appended token's position has no row in the rotation table (skipped) */
+    MLA_ERR_PAGE = 8           /* device: a block-table entry that a call needed was outside [0, num_pages): read
+                                  as rows of zeros, or the token not written; the sequence's results are invalid */
 } mla_status;
 
 /* Kernel variants a plan can select. */
@@ -96,7 +99,13 @@ typedef struct mla_plan {
     int32_t Hkv;               /* kv heads: 1 for MLA (one latent cache); MHA: query head h reads kv head
                                   h / (H / Hkv) */
     int32_t head_dim;          /* width of a key row: 576 (MLA), 128 (MHA) */
-    uint64_t reserved[4];
+    int32_t page_size;         /* paged plans: rows per cache page; 0: a contiguous cache */
+    int32_t window;            /* paged plans: sliding window, 0 = none */
+    int32_t first_tokens;      /* paged plans with a window: first tokens that stay visible */
+    int32_t prefix_max;        /* shared-prefix plans: most prefix keys; 0: no prefix */
+    int32_t prefix_partitions; /* shared-prefix plans: KV partitions of the prefix's launch */
+    int32_t prefix_groups;     /* shared-prefix plans: 128-row groups of the batch's query rows */
+    uint64_t reserved[1];
 } mla_plan;
 
 /*
@@ -410,6 +419,156 @@ mla_status mla_decode_run_fp8(const mla_plan* plan, const void* q, const void* k
 mla_status mla_decode_run_fp8_phase(const mla_plan* plan, const void* q, const void* kv_fp8, float kv_scale,
                                     const int32_t* seqlens, float softmax_scale, void* out, float* lse,
                                     void* workspace, size_t workspace_bytes, void* stream, int32_t phase);
+
+/*
+ * The cache in pages.  A latent cache of num_pages pages of page_size rows,
+ * bf16 [num_pages, page_size, 576] (keys and values as above); key j of
+ * sequence b is row j % page_size of page block_table[b][j / page_size].  For
+ * grouped kv heads, k_pages and v_pages are bf16 [num_pages, page_size, Hkv, 128].
+ *
+ * Visibility.  Query token t of a sequence of L = seqlens[b] keys is at
+ * position p = L - Sq + t and sees the keys
+ *     j <= p   with   j > p - window  or  j < first_tokens
+ * (window 0: every j <= p).  first_tokens are the first tokens of a sequence
+ * that stay visible when the window has moved on; they are keys with values,
+ * unlike the sink logits of `sinks`, and both may be used together.  A token
+ * that sees nothing (p < 0) has out = 0 and lse = -inf, or its head's sink.
+ * Only the pages that hold a visible key are looked up, and rows that no token
+ * of the sequence sees (NaN or anything else) do not enter the result.  A value
+ * that is not finite in a row that one token sees reaches the others as well.
+ *
+ * mla_decode_plan_paged -- as mla_decode_plan for such a cache:
+ *   page_size     a multiple of 16 up to 2^24 (else MLA_ERR_UNSUPPORTED for
+ *                 other sizes in [1, 2^24]); multiples of 64 load fastest
+ *   window        >= 0, 0 = none;  first_tokens  in [0, 2^24], used with a window
+ * mha_decode_plan_paged -- as mha_decode_plan, with the same three.
+ * mla_decode_plan_paged_fp8 -- the same for pages of E4M3 codes; the plan's kernel
+ * is MLA_KERNEL_FP8_MMA at every shape.
+ */
+mla_status mla_decode_plan_paged(int32_t B, int32_t Sq, int32_t H, int32_t L_max, int32_t page_size, int32_t window,
+                                 int32_t first_tokens, int32_t device, int32_t num_partitions_override,
+                                 mla_plan* plan, size_t* workspace_bytes);
+mla_status mla_decode_plan_paged_fp8(int32_t B, int32_t Sq, int32_t H, int32_t L_max, int32_t page_size,
+                                     int32_t window, int32_t first_tokens, int32_t device,
+                                     int32_t num_partitions_override, mla_plan* plan, size_t* workspace_bytes);
+mla_status mha_decode_plan_paged(int32_t B, int32_t Sq, int32_t H, int32_t Hkv, int32_t L_max, int32_t page_size,
+                                 int32_t window, int32_t first_tokens, int32_t device,
+                                 int32_t num_partitions_override, mla_plan* plan, size_t* workspace_bytes);
+
+/*
+ * mla_decode_run_paged, mla_decode_run_paged_fp8, mha_decode_run_paged -- enqueue
+ * one decode over a paged cache.
+ *   kv_pages (k_pages, v_pages)  device, as above, contiguous, 16-byte aligned
+ *   num_pages     pages of the cache, >= 1
+ *   block_table   device, int32, row b at block_table + b * table_stride;
+ *                 table_width entries of a row may be read, and
+ *                 table_width * page_size >= L_max.  Entries of pages without a
+ *                 visible key are not read.  An entry outside [0, num_pages)
+ *                 that is needed is read as a page of zeros and flagged
+ *                 (MLA_ERR_PAGE from mla_decode_check).
+ *   sinks         as mla_decode_run_sinks, or NULL
+ *   kv_scale      E4M3 pages: as mla_decode_run_fp8
+ * Every other argument, the launches and the return codes are those of
+ * mla_decode_run (mha_decode_run); MLA_ERR_INVALID_ARG for a plan of another kind.
+ */
+mla_status mla_decode_run_paged(const mla_plan* plan, const void* q, const void* kv_pages, int32_t num_pages,
+                                const int32_t* block_table, int64_t table_stride, int32_t table_width,
+                                const int32_t* seqlens, float softmax_scale, const float* sinks, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream);
+mla_status mla_decode_run_paged_fp8(const mla_plan* plan, const void* q, const void* kv_pages, int32_t num_pages,
+                                    float kv_scale, const int32_t* block_table, int64_t table_stride,
+                                    int32_t table_width, const int32_t* seqlens, float softmax_scale,
+                                    const float* sinks, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+mla_status mha_decode_run_paged(const mla_plan* plan, const void* q, const void* k_pages, const void* v_pages,
+                                int32_t num_pages, const int32_t* block_table, int64_t table_stride,
+                                int32_t table_width, const int32_t* seqlens, float softmax_scale, const float* sinks,
+                                void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Shared prefix.  All sequences of the batch start with the same prefix_len
+ * keys (a system prompt, one prompt sampled many times), held once in the
+ * cache; the batch attends to them once, 128 query rows of any sequences at a
+ * time, instead of once per sequence.  seqlens[b] counts the sequence's own
+ * keys, which follow the prefix and are in block_table:
+ *     every query token sees every prefix key;
+ *     token t sees the own keys j <= seqlens[b] - Sq + t.
+ * The result is the softmax over both.  A sequence without own keys
+ * (seqlens[b] = 0) sees the prefix; with prefix_len = 0 as well its rows are empty.
+ *
+ * mla_decode_plan_prefix -- as mla_decode_plan_paged without a window:
+ *   L_max       most own keys of a sequence;  prefix_max  most prefix keys (1..2^24)
+ * The workspace holds one fp32 partial per query row for the prefix and one
+ * for its own keys, besides those of cut pieces.
+ *
+ * mla_decode_run_prefix -- enqueue one such decode.
+ *   prefix_table  device, int32, the prefix's pages in order, prefix_width
+ *                 entries, prefix_width * page_size >= prefix_max
+ *   prefix_len    device, one int32 in [0, prefix_max] (else clamped and flagged)
+ * Other arguments and return codes as mla_decode_run_paged.
+ */
+mla_status mla_decode_plan_prefix(int32_t B, int32_t Sq, int32_t H, int32_t L_max, int32_t prefix_max,
+                                  int32_t page_size, int32_t device, int32_t num_partitions_override, mla_plan* plan,
+                                  size_t* workspace_bytes);
+mla_status mla_decode_run_prefix(const mla_plan* plan, const void* q, const void* kv_pages, int32_t num_pages,
+                                 const int32_t* prefix_table, int32_t prefix_width, const int32_t* prefix_len,
+                                 const int32_t* block_table, int64_t table_stride, int32_t table_width,
+                                 const int32_t* seqlens, float softmax_scale, const float* sinks, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Appending new tokens to a paged cache, with the position rotation applied
+ * on the way.  The new tokens of all sequences are laid end to end; token i
+ * belongs to the sequence b with cu_tokens[b] <= i < cu_tokens[b + 1] and is at
+ * position p = seqlens[b] - (cu_tokens[b + 1] - cu_tokens[b]) + i - cu_tokens[b]:
+ * seqlens are the lengths with the new tokens, the ones the decode after it is
+ * given.  A rotated row x of n columns turns by the angles of p, in fp32:
+ *     (x0, x1) -> (x0 c - x1 s, x1 c + x0 s),  c = cos_sin[p][i], s = cos_sin[p][n/2 + i]
+ * with the pairs (2i, 2i+1) (interleaved = 1) or (i, i + n/2) (0), and is
+ * rounded once, to bf16 or to E4M3.
+ *
+ * A token outside every [cu_tokens[b], cu_tokens[b + 1]) is padding and is
+ * left alone.  A token whose position is outside [0, num_positions) is skipped
+ * and flagged (MLA_ERR_SEQLEN); one whose page is outside the table's width or
+ * [0, num_pages) has its queries rotated, its cache row not written, and is
+ * flagged (MLA_ERR_PAGE).  Two tokens with the same place leave either's row.
+ */
+typedef struct mla_append {
+    int32_t B, T;               /* sequences (>= 1), new tokens of all of them (>= 0) */
+    int32_t H, Hkv;             /* query heads to rotate (0: none); kv heads (mha_cache_append) */
+    int32_t rope_dim;           /* rotated columns of a row: 64 (mla_cache_append: all of the rope part), or a
+                                   multiple of 16 up to 128 (mha_cache_append: the first ones; the rest is copied) */
+    int32_t interleaved;        /* 0 or 1 */
+    int32_t num_positions;      /* rows of cos_sin */
+    int32_t page_size, num_pages, table_width;
+    int64_t table_stride;       /* elements */
+    const int32_t* cu_tokens;   /* device [B + 1], or NULL: T / B tokens each (T % B == 0) */
+    const int32_t* seqlens;     /* device [B] */
+    const int32_t* block_table; /* device, as for mla_decode_run_paged; page_size is any size >= 1 here */
+    const float* cos_sin;       /* device fp32 [num_positions, rope_dim]: cosines, then sines; 16-byte aligned */
+    const void* k;              /* device bf16: mla: the latent [T, 512]; mha: keys [T, Hkv, 128] */
+    const void* v;              /* device bf16: mla: the key's rope part [T, 64]; mha: values [T, Hkv, 128] */
+    const void* q_in;           /* device bf16: mla: the queries' rope part [T, H, 64]; mha: queries [T, H, 128] */
+    void* q_out;                /* device bf16, same shape: the rotated rows (mla: columns 512.. of a [T, H, 576]
+                                   tensor, whose pointer this is, plus 512).  May be q_in. */
+    void* k_pages;              /* device: mla: the latent cache; mha: the key pages */
+    void* v_pages;              /* device: mha: the value pages */
+    /* element strides, multiples of 8 (rows are 16-byte aligned, columns contiguous) */
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int64_t q_in_token_stride, q_in_head_stride, q_out_token_stride, q_out_head_stride;
+    uint32_t* status;           /* device status word (a decode workspace's first), or NULL: faults not recorded */
+    float kv_scale;             /* mla: 0: the cache is bf16; > 0: it holds E4M3 codes of row / kv_scale, saturated
+                                   at +-448 (for mla_decode_run_paged_fp8, or mla_decode_run_fp8 where a
+                                   sequence is one page) */
+    int32_t reserved;
+} mla_append;
+
+/* Enqueue the append of latent rows (576 wide).  One launch, none for T = 0
+ * (k, v, q_in and q_out may be NULL then);
+ * MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_ALIGNMENT, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA. */
+mla_status mla_cache_append(const mla_append* args, void* stream);
+/* Enqueue the append of keys and values of grouped kv heads (128 wide, bf16); as mla_cache_append. */
+mla_status mha_cache_append(const mla_append* args, void* stream);
 
 /* Static English description of a status code (never NULL). */
 const char* mla_status_string(mla_status status);

@@ -8,7 +8,11 @@ device is not an sm_100 GPU, the calls raise.
 Entry points mirror include/mla_decode.h:
     mla_decode_plan, mla_decode_workspace_init, mla_decode_run,
     mla_decode_check, mla_status_string, mla_decode_set_debug,
-    mla_decode_run_noalloc, mla_decode_run_sinks
+    mla_decode_run_noalloc, mla_decode_run_sinks,
+    the paged cache's mla_decode_plan_paged, mla_decode_run_paged,
+    mla_decode_plan_paged_fp8, mla_decode_run_paged_fp8,
+    mha_decode_plan_paged, mha_decode_run_paged, mla_decode_plan_prefix,
+    mla_decode_run_prefix, mla_cache_append, mha_cache_append
 plus the convenience wrappers ``mla_decode`` (device tensors in, device
 tensors out) and ``mla_decode_host`` (host tensors in and out, with the
 copies done here around the library call).
@@ -17,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Tuple
 
@@ -29,7 +34,8 @@ D_V = 512
 
 MLA_OK = 0
 STATUS_NAMES = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_ALIGNMENT", 3: "MLA_ERR_UNSUPPORTED",
-                4: "MLA_ERR_CUDA", 5: "MLA_ERR_TIMEOUT", 6: "MLA_ERR_WORKSPACE", 7: "MLA_ERR_SEQLEN"}
+                4: "MLA_ERR_CUDA", 5: "MLA_ERR_TIMEOUT", 6: "MLA_ERR_WORKSPACE", 7: "MLA_ERR_SEQLEN",
+                8: "MLA_ERR_PAGE"}
 MLA_KERNEL_TRANSPOSED = 1
 MLA_KERNEL_PAIR = 2
 MLA_KERNEL_MHA = 3
@@ -44,7 +50,10 @@ EXPORTED_SYMBOLS = ("mla_decode_plan", "mla_decode_plan_kernel", "mla_decode_pla
                     "mla_status_string", "mla_decode_abi_version", "mla_decode_set_debug",
                     "mha_decode_plan", "mha_decode_run", "mha_decode_run_phase",
                     "mla_decode_plan_fp8", "mla_decode_plan_fp8_kernel", "mla_decode_run_fp8",
-                    "mla_decode_run_fp8_phase")
+                    "mla_decode_run_fp8_phase",
+                    "mla_decode_plan_paged", "mla_decode_run_paged", "mla_decode_plan_paged_fp8",
+                    "mla_decode_run_paged_fp8", "mha_decode_plan_paged", "mha_decode_run_paged",
+                    "mla_decode_plan_prefix", "mla_decode_run_prefix", "mla_cache_append", "mha_cache_append")
 
 
 class MlaError(RuntimeError):
@@ -61,7 +70,10 @@ class mla_plan(ctypes.Structure):
                 ("smem_bytes", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64),
                 ("l2_prefetch_tiles", ctypes.c_int32), ("split_tiles", ctypes.c_int32),
                 ("Hkv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
-                ("reserved", ctypes.c_uint64 * 4)]
+                ("page_size", ctypes.c_int32), ("window", ctypes.c_int32), ("first_tokens", ctypes.c_int32),
+                ("prefix_max", ctypes.c_int32), ("prefix_partitions", ctypes.c_int32),
+                ("prefix_groups", ctypes.c_int32),
+                ("reserved", ctypes.c_uint64 * 1)]
 
     def as_dict(self):
         return {k: getattr(self, k) for k, _ in self._fields_ if not k.startswith("reserved")}
@@ -132,6 +144,22 @@ def load_library(build_if_missing: bool = True):
         lib.mla_decode_run_fp8_phase.restype = c_i32
         lib.mla_decode_run_fp8_phase.argtypes = [ctypes.POINTER(mla_plan), c_vp, c_vp, c_f, c_vp, c_f, c_vp, c_vp,
                                                  c_vp, c_sz, c_vp, c_i32]
+        pp, ps, c_i64 = ctypes.POINTER(mla_plan), ctypes.POINTER(c_sz), ctypes.c_int64
+        lib.mla_decode_plan_paged.argtypes = [c_i32] * 9 + [pp, ps]
+        lib.mla_decode_plan_paged_fp8.argtypes = [c_i32] * 9 + [pp, ps]
+        lib.mha_decode_plan_paged.argtypes = [c_i32] * 10 + [pp, ps]
+        lib.mla_decode_plan_prefix.argtypes = [c_i32] * 8 + [pp, ps]
+        tail = [c_vp, c_i64, c_i32, c_vp, c_f, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]  # block_table .. stream
+        lib.mla_decode_run_paged.argtypes = [pp, c_vp, c_vp, c_i32] + tail
+        lib.mla_decode_run_paged_fp8.argtypes = [pp, c_vp, c_vp, c_i32, c_f] + tail
+        lib.mha_decode_run_paged.argtypes = [pp, c_vp, c_vp, c_vp, c_i32] + tail
+        lib.mla_decode_run_prefix.argtypes = [pp, c_vp, c_vp, c_i32, c_vp, c_i32, c_vp] + tail
+        lib.mla_cache_append.argtypes = [c_vp, c_vp]
+        lib.mha_cache_append.argtypes = [c_vp, c_vp]
+        for fn in (lib.mla_decode_plan_paged, lib.mha_decode_plan_paged, lib.mla_decode_plan_prefix,
+                   lib.mla_decode_plan_paged_fp8, lib.mla_decode_run_paged_fp8, lib.mla_decode_run_paged, lib.mha_decode_run_paged, lib.mla_decode_run_prefix,
+                   lib.mla_cache_append, lib.mha_cache_append):
+            fn.restype = c_i32
         lib.mla_decode_check.restype = c_i32
         lib.mla_decode_check.argtypes = [ctypes.POINTER(mla_plan), c_vp, c_vp]
         lib.mla_status_string.restype = ctypes.c_char_p
@@ -464,3 +492,302 @@ def mla_decode_run_fp8_phase(plan: mla_plan, q: torch.Tensor, kv_fp8: torch.Tens
                                                  workspace.numel(), _stream_handle(stream), int(phase))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_decode_run_fp8_phase")
+
+
+# ---------------------------------------------------------------- paged cache
+
+def mla_decode_plan_paged(B: int, Sq: int, H: int, L_max: int, page_size: int, window: int = 0,
+                          first_tokens: int = 0, device: Optional[int] = None, num_partitions: int = 0) -> mla_plan:
+    """A plan for a latent cache in pages: query token t of a sequence of L keys
+    sees the keys up to its position p = L - Sq + t, and with a window those of
+    the last `window` positions or the `first_tokens` first ones."""
+    if device is None:
+        device = torch.cuda.current_device()
+    p = mla_plan()
+    rc = load_library().mla_decode_plan_paged(int(B), int(Sq), int(H), int(L_max), int(page_size), int(window),
+                                              int(first_tokens), int(device), int(num_partitions), ctypes.byref(p),
+                                              None)
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_decode_plan_paged")
+    return p
+
+
+def mla_decode_plan_paged_fp8(B: int, Sq: int, H: int, L_max: int, page_size: int, window: int = 0,
+                              first_tokens: int = 0, device: Optional[int] = None,
+                              num_partitions: int = 0) -> mla_plan:
+    """mla_decode_plan_paged for pages of E4M3 codes with one dequantisation scale."""
+    if device is None:
+        device = torch.cuda.current_device()
+    p = mla_plan()
+    rc = load_library().mla_decode_plan_paged_fp8(int(B), int(Sq), int(H), int(L_max), int(page_size), int(window),
+                                                  int(first_tokens), int(device), int(num_partitions),
+                                                  ctypes.byref(p), None)
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_decode_plan_paged_fp8")
+    return p
+
+
+def mha_decode_plan_paged(B: int, Sq: int, H: int, Hkv: int, L_max: int, page_size: int, window: int = 0,
+                          first_tokens: int = 0, device: Optional[int] = None, num_partitions: int = 0) -> mla_plan:
+    """mla_decode_plan_paged for key and value pages of grouped kv heads (128 wide)."""
+    if device is None:
+        device = torch.cuda.current_device()
+    p = mla_plan()
+    rc = load_library().mha_decode_plan_paged(int(B), int(Sq), int(H), int(Hkv), int(L_max), int(page_size),
+                                              int(window), int(first_tokens), int(device), int(num_partitions),
+                                              ctypes.byref(p), None)
+    if rc != MLA_OK:
+        raise MlaError(rc, "mha_decode_plan_paged")
+    return p
+
+
+def mla_decode_plan_prefix(B: int, Sq: int, H: int, L_max: int, prefix_max: int, page_size: int,
+                           device: Optional[int] = None, num_partitions: int = 0) -> mla_plan:
+    """A plan for a batch that shares a prefix of at most prefix_max keys; L_max
+    is the most own keys a sequence has after it."""
+    if device is None:
+        device = torch.cuda.current_device()
+    p = mla_plan()
+    rc = load_library().mla_decode_plan_prefix(int(B), int(Sq), int(H), int(L_max), int(prefix_max), int(page_size),
+                                               int(device), int(num_partitions), ctypes.byref(p), None)
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_decode_plan_prefix")
+    return p
+
+
+def _check_table(t: torch.Tensor, name: str, rows: Optional[int]) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if t.dim() != (1 if rows is None else 2) or (rows is not None and t.shape[0] != rows) or t.shape[-1] < 1:
+        raise ValueError(f"{name} must have shape {'(width,)' if rows is None else f'({rows}, width)'}, "
+                         f"got {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the entries of a row must be contiguous")
+
+
+def _check_device(device, tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors must be on {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current device")
+
+
+def _check_paged(plan, q, pages, seqlens, block_table, out, lse, sinks, workspace, d_key, d_value, page_row,
+                 dtype=torch.bfloat16):
+    B, Sq, H = plan.B, plan.Sq, plan.H
+    _check_tensor(q, "q", torch.bfloat16, (B, Sq, H, d_key))
+    for name, p in pages:
+        _check_tensor(p, name, dtype, (p.shape[0], plan.page_size, *page_row))
+    _check_tensor(seqlens, "seqlens", torch.int32, (B,))
+    _check_table(block_table, "block_table", B)
+    _check_tensor(out, "out", torch.bfloat16, (B, Sq, H, d_value))
+    _check_tensor(lse, "lse", torch.float32, (B, Sq, H))
+    if sinks is not None:
+        _check_tensor(sinks, "sinks", torch.float32, (H,))
+    _check_device(q.device, (seqlens, block_table, out, lse, sinks, workspace, *(p for _, p in pages)))
+
+
+def mla_decode_run_paged(plan: mla_plan, q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tensor,
+                         seqlens: torch.Tensor, softmax_scale: float, out: torch.Tensor, lse: torch.Tensor,
+                         workspace: torch.Tensor, sinks: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Enqueue one decode over a paged cache: kv_pages bf16 [pages, page_size,
+    576], block_table int32 [B, width] (rows may be strided), seqlens the
+    lengths with the query tokens' own keys."""
+    _check_paged(plan, q, (("kv_pages", kv_pages),), seqlens, block_table, out, lse, sinks, workspace, D_QK, D_V,
+                 (D_QK,))
+    rc = load_library().mla_decode_run_paged(ctypes.byref(plan), q.data_ptr(), kv_pages.data_ptr(), kv_pages.shape[0],
+                                             block_table.data_ptr(), block_table.stride(0), block_table.shape[1],
+                                             seqlens.data_ptr(), float(softmax_scale),
+                                             sinks.data_ptr() if sinks is not None else None, out.data_ptr(),
+                                             lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                             _stream_handle(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_decode_run_paged")
+
+
+def mla_decode_run_paged_fp8(plan: mla_plan, q: torch.Tensor, kv_pages: torch.Tensor, kv_scale: float,
+                             block_table: torch.Tensor, seqlens: torch.Tensor, softmax_scale: float,
+                             out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor,
+                             sinks: Optional[torch.Tensor] = None, stream=None) -> None:
+    """mla_decode_run_paged over pages of E4M3 codes (torch.uint8 or
+    torch.float8_e4m3fn) that stand for code * kv_scale."""
+    pages = _fp8_codes(kv_pages)
+    _check_paged(plan, q, (("kv_pages", pages),), seqlens, block_table, out, lse, sinks, workspace, D_QK, D_V,
+                 (D_QK,), torch.uint8)
+    rc = load_library().mla_decode_run_paged_fp8(ctypes.byref(plan), q.data_ptr(), pages.data_ptr(), pages.shape[0],
+                                                 float(kv_scale), block_table.data_ptr(), block_table.stride(0),
+                                                 block_table.shape[1], seqlens.data_ptr(), float(softmax_scale),
+                                                 sinks.data_ptr() if sinks is not None else None, out.data_ptr(),
+                                                 lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                                 _stream_handle(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_decode_run_paged_fp8")
+
+
+def mha_decode_run_paged(plan: mla_plan, q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                         block_table: torch.Tensor, seqlens: torch.Tensor, softmax_scale: float, out: torch.Tensor,
+                         lse: torch.Tensor, workspace: torch.Tensor, sinks: Optional[torch.Tensor] = None,
+                         stream=None) -> None:
+    """Enqueue one MHA decode over key and value pages bf16 [pages, page_size, Hkv, 128]."""
+    if v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape")
+    _check_paged(plan, q, (("k_pages", k_pages), ("v_pages", v_pages)), seqlens, block_table, out, lse, sinks,
+                 workspace, MHA_D, MHA_D, (plan.Hkv, MHA_D))
+    rc = load_library().mha_decode_run_paged(ctypes.byref(plan), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                             k_pages.shape[0], block_table.data_ptr(), block_table.stride(0),
+                                             block_table.shape[1], seqlens.data_ptr(), float(softmax_scale),
+                                             sinks.data_ptr() if sinks is not None else None, out.data_ptr(),
+                                             lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                             _stream_handle(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mha_decode_run_paged")
+
+
+def mla_decode_run_prefix(plan: mla_plan, q: torch.Tensor, kv_pages: torch.Tensor, prefix_table: torch.Tensor,
+                          prefix_len: torch.Tensor, block_table: torch.Tensor, seqlens: torch.Tensor,
+                          softmax_scale: float, out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor,
+                          sinks: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Enqueue one decode of a batch with a shared prefix: prefix_table int32
+    [width] the prefix's pages, prefix_len int32 [1] on the device, seqlens the
+    sequences' own keys (the query tokens' among them), found in block_table."""
+    _check_paged(plan, q, (("kv_pages", kv_pages),), seqlens, block_table, out, lse, sinks, workspace, D_QK, D_V,
+                 (D_QK,))
+    _check_table(prefix_table, "prefix_table", None)
+    _check_tensor(prefix_len, "prefix_len", torch.int32, (1,))
+    _check_device(q.device, (prefix_table, prefix_len))
+    rc = load_library().mla_decode_run_prefix(ctypes.byref(plan), q.data_ptr(), kv_pages.data_ptr(), kv_pages.shape[0],
+                                              prefix_table.data_ptr(), prefix_table.shape[0], prefix_len.data_ptr(),
+                                              block_table.data_ptr(), block_table.stride(0), block_table.shape[1],
+                                              seqlens.data_ptr(), float(softmax_scale),
+                                              sinks.data_ptr() if sinks is not None else None, out.data_ptr(),
+                                              lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                              _stream_handle(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_decode_run_prefix")
+
+
+def rope_table(num_positions: int, dim: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """The rotation table of the append calls: fp32 [num_positions, dim], row p
+    the cosines, then the sines, of p * base^(-2i/dim), computed in 64 bits."""
+    inv = base ** (-torch.arange(0, dim, 2, dtype=torch.float64, device=device) / dim)
+    angle = torch.arange(num_positions, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat([angle.cos(), angle.sin()], dim=1).float()
+
+
+_APPEND = struct.Struct("=10iq10Q8qQfi")  # the fields of mla_append, in order
+
+
+def _check_rows(t: torch.Tensor, name: str, shape) -> None:
+    """bf16 rows [T, (heads,) width]: any strides but the last."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
+def _strides(t: Optional[torch.Tensor]) -> Tuple[int, int]:
+    """(token, head) element strides; 0 where there is one token or head (or no head axis)."""
+    if t is None:
+        return 0, 0
+    return (t.stride(0) if t.shape[0] > 1 else 0,
+            t.stride(1) if t.dim() == 3 and t.shape[1] > 1 else 0)
+
+
+def _append(name, k, v, cos_sin, k_pages, v_pages, block_table, seqlens, cu_tokens, q_in, q_out, q_out_offset,
+            kv_scale, interleaved, workspace, stream, Hkv):
+    T, B = k.shape[0], seqlens.shape[0]
+    _check_tensor(seqlens, "seqlens", torch.int32, (B,))
+    _check_table(block_table, "block_table", B)
+    _check_tensor(cos_sin, "cos_sin", torch.float32, cos_sin.shape)
+    if cos_sin.dim() != 2:
+        raise ValueError(f"cos_sin must have shape (positions, rotated columns), got {tuple(cos_sin.shape)}")
+    if cu_tokens is not None:
+        _check_tensor(cu_tokens, "cu_tokens", torch.int32, (B + 1,))
+    H = 0
+    if q_in is not None:
+        H = q_in.shape[1]
+        for i in range(2):
+            if q_out.shape[i] > 1 and q_out.stride(i) == 0:
+                raise ValueError("the rotated queries' rows must not share memory")
+    elif q_out is not None:
+        raise ValueError("rotated queries need both their input and their output")
+    _check_device(k.device, (v, cos_sin, k_pages, v_pages, block_table, seqlens, cu_tokens, q_in, q_out, workspace))
+    args = _APPEND.pack(
+        B, T, H, Hkv, cos_sin.shape[1], 1 if interleaved else 0, cos_sin.shape[0], k_pages.shape[1],
+        k_pages.shape[0], block_table.shape[1], block_table.stride(0),
+        cu_tokens.data_ptr() if cu_tokens is not None else 0, seqlens.data_ptr(), block_table.data_ptr(),
+        cos_sin.data_ptr(), k.data_ptr(), v.data_ptr(), q_in.data_ptr() if H else 0,
+        q_out.data_ptr() + q_out_offset if H else 0, k_pages.data_ptr(),
+        v_pages.data_ptr() if v_pages is not None else 0, *_strides(k), *_strides(v), *_strides(q_in),
+        *_strides(q_out), workspace.data_ptr() if workspace is not None else 0, kv_scale, 0)
+    lib = load_library()
+    rc = getattr(lib, name)(args, _stream_handle(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, name)
+
+
+def mla_cache_append(latent: torch.Tensor, k_rope: torch.Tensor, cos_sin: torch.Tensor, kv_pages: torch.Tensor,
+                     block_table: torch.Tensor, seqlens: torch.Tensor, cu_tokens: Optional[torch.Tensor] = None,
+                     q_rope: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                     kv_scale: Optional[float] = None, interleaved: bool = True,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Append T new tokens to a latent cache: latent bf16 [T, 512] and the
+    rotated k_rope bf16 [T, 64] become cache rows of kv_pages [pages, page_size,
+    576] (bf16, or E4M3 codes of row / kv_scale), and the rotated q_rope bf16
+    [T, H, 64] becomes columns 512.. of q [T, H, 576].
+
+    cos_sin: fp32 [positions, 64] (rope_table).  seqlens int32 [B]: lengths with
+    the new tokens; cu_tokens int32 [B + 1]: where each sequence's tokens start
+    (None: T / B tokens each).  With a decode workspace, tokens without a
+    position or page are reported by mla_decode_check.  A contiguous cache
+    [B, L_max, 576] is a paged one with block_table[b] = [b]."""
+    T = latent.shape[0]
+    _check_rows(latent, "latent", (T, D_V))
+    _check_rows(k_rope, "k_rope", (T, D_QK - D_V))
+    fp8 = kv_pages.dtype in (torch.uint8, torch.float8_e4m3fn)
+    if fp8 != (kv_scale is not None):
+        raise ValueError("kv_scale goes with a cache of E4M3 codes (torch.uint8 or torch.float8_e4m3fn)")
+    if fp8 and not kv_scale > 0:
+        raise ValueError("kv_scale must be positive")
+    pages = _fp8_codes(kv_pages) if fp8 else kv_pages
+    _check_tensor(pages, "kv_pages", torch.uint8 if fp8 else torch.bfloat16, (*pages.shape[:2], D_QK))
+    if cos_sin.shape[-1] != D_QK - D_V:
+        raise ValueError(f"cos_sin must have shape (positions, {D_QK - D_V}), got {tuple(cos_sin.shape)}")
+    if q_rope is not None:
+        if q is None:
+            raise ValueError("rotated queries need both their input and their output")
+        _check_rows(q_rope, "q_rope", (T, q_rope.shape[1] if q_rope.dim() == 3 else -1, D_QK - D_V))
+        _check_rows(q, "q", (T, q_rope.shape[1], D_QK))
+    _append("mla_cache_append", latent, k_rope, cos_sin, pages, None, block_table, seqlens, cu_tokens, q_rope, q,
+            2 * D_V, float(kv_scale) if fp8 else 0.0, interleaved, workspace, stream, 1)
+
+
+def mha_cache_append(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor, k_pages: torch.Tensor,
+                     v_pages: torch.Tensor, block_table: torch.Tensor, seqlens: torch.Tensor,
+                     cu_tokens: Optional[torch.Tensor] = None, q_in: Optional[torch.Tensor] = None,
+                     q_out: Optional[torch.Tensor] = None, interleaved: bool = False,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Append T new tokens' keys (rotated) and values, bf16 [T, Hkv, 128], to
+    k_pages and v_pages [pages, page_size, Hkv, 128], and rotate the queries
+    q_in [T, H, 128] into q_out (which may be q_in).  cos_sin: fp32 [positions,
+    n], n a multiple of 16 up to 128: the first n columns turn, the rest is
+    copied.  Other arguments as mla_cache_append."""
+    T, Hkv = k.shape[0], k.shape[1] if k.dim() == 3 else -1
+    _check_rows(k, "k", (T, Hkv, MHA_D))
+    _check_rows(v, "v", (T, Hkv, MHA_D))
+    _check_tensor(k_pages, "k_pages", torch.bfloat16, (*k_pages.shape[:2], Hkv, MHA_D))
+    _check_tensor(v_pages, "v_pages", torch.bfloat16, k_pages.shape)
+    if q_in is not None:
+        if q_out is None:
+            raise ValueError("rotated queries need both their input and their output")
+        _check_rows(q_in, "q_in", (T, q_in.shape[1] if q_in.dim() == 3 else -1, MHA_D))
+        _check_rows(q_out, "q_out", q_in.shape)
+    _append("mha_cache_append", k, v, cos_sin, k_pages, v_pages, block_table, seqlens, cu_tokens, q_in, q_out, 0, 0.0,
+            interleaved, workspace, stream, Hkv)

@@ -1,0 +1,317 @@
+// kernel_append.cuh -- appending new tokens to a paged cache with the
+// position rotation applied on the way.
+//
+// Token i of the flattened new tokens belongs to the sequence b with
+// cu[b] <= i < cu[b+1] and sits at position p = L_b - n_b + (i - cu[b])
+// (L_b: the sequence's length with its new tokens, n_b = cu[b+1] - cu[b]).  Its
+// row goes to page table[b][p / page_size], row p % page_size; the row's
+// rotated columns, and the token's query rows, turn by the angles of p:
+//     (x0, x1) -> (x0 c - x1 s, x1 c + x0 s),   c, s = cos_sin[p]
+// with pairs (2i, 2i+1) (interleaved) or (i, i + n/2).  All of it is fp32,
+// rounded once when it is written (products and sums each rounded, no fused
+// multiply-add, so the result is the one elementary operations give).
+//
+// Bound by HBM: every input is read once and every output written once, and a
+// token needs only its own rows.  A warp takes one task -- a token's cache row,
+// or 8 (128 wide) / 16 (64 wide) head rows of it, about 2 KB -- with all of its
+// 16-byte loads issued before the position is known, so the dependent chain
+// (which sequence, its length, its angles) overlaps them; a prefill has some
+// 10^4 tasks, enough to cover the latency with occupancy alone.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cstdint>
+
+#include "paged.cuh"
+#include "schedule.cuh"
+
+namespace mla {
+
+
+struct AppendArgs {
+    int B, T;
+    int per_seq;                // tokens of every sequence when cu is null
+    const int32_t* cu;          // [B + 1] or null
+    const int32_t* seqlens;     // [B], with the new tokens
+    const int32_t* table;
+    long long table_stride;
+    int table_width, num_pages, page_size;
+    const float* cos_sin;       // [num_positions, rot]: rot / 2 cosines, rot / 2 sines
+    int num_positions, rot;
+    uint32_t* status;           // or null
+    // head rows: key rows (MHA), value rows (MHA), query rows; element strides
+    const __nv_bfloat16* k;     // MLA: latent [T, 512]
+    long long k_token, k_head;
+    const __nv_bfloat16* v;     // MLA: k_rope [T, 64]
+    long long v_token, v_head;
+    const __nv_bfloat16* q_in;  // or null
+    long long qi_token, qi_head;
+    __nv_bfloat16* q_out;
+    long long qo_token, qo_head;
+    int H, Hkv;
+    void* k_pages;              // MLA: the cache's rows of 576
+    __nv_bfloat16* v_pages;
+    float kv_scale;             // E4M3 cache
+};
+
+constexpr int kAppendThreads = 128;
+constexpr int kAppendRowBytes = 2048;  // head-row bytes of one task
+
+// The sequence of token i (cu[b] <= i < cu[b+1]), or -1; warp-cooperative.
+// Each round narrows the range 32-fold: the lanes read evenly spaced bounds
+// and the last one at most i opens the next range.
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int i, int lane) {
+    int lo = 0, n = B + 1;  // the answer's index is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) >> 5;
+        const int at = lane * step;
+        const bool le = at < n && __ldg(cu + lo + at) <= i;
+        const unsigned m = __ballot_sync(0xffffffffu, le);
+        if (m == 0) return -1;
+        const int last = 31 - __clz(m);
+        lo += last * step;
+        n = n - last * step < step ? n - last * step : step;
+    }
+    return lo < B && __ldg(cu + lo) <= i && i < __ldg(cu + lo + 1) ? lo : -1;
+}
+
+// Sequence and position of token i; position -1: the token is in no sequence
+// (padding) or its position is outside [0, num_positions) (flagged).
+__device__ __forceinline__ void place_token(const AppendArgs& a, int i, int lane, int& b, int& pos) {
+    int first, n;
+    if (a.cu) {
+        b = sequence_of(a.cu, a.B, i, lane);
+        if (b < 0) {
+            pos = -1;
+            return;
+        }
+        first = __ldg(a.cu + b);
+        n = __ldg(a.cu + b + 1) - first;
+    } else {
+        b = i / a.per_seq;
+        first = b * a.per_seq;
+        n = a.per_seq;
+    }
+    const long long p = static_cast<long long>(__ldg(a.seqlens + b)) - n + (i - first);
+    pos = -1;
+    if (p >= 0 && p < a.num_positions) pos = static_cast<int>(p);
+    else if (a.status && lane == 0) atomicOr(a.status, kStatusSeqlen);
+}
+
+// Row of the cache for position pos of sequence b, or -1 (flagged).
+__device__ __forceinline__ long long cache_row(const AppendArgs& a, int b, int pos, int lane) {
+    const int e = pos / a.page_size;
+    int page = -1;
+    if (e < a.table_width) page = __ldg(a.table + b * a.table_stride + e);
+    if (page < 0 || page >= a.num_pages) {
+        if (a.status && lane == 0) atomicOr(a.status, kStatusPage);
+        return -1;
+    }
+    return static_cast<long long>(page) * a.page_size + (pos - e * a.page_size);
+}
+
+__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Eight E4M3 codes of x / scale, saturated at +-448 (round to nearest even).
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale) {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 y = make_float2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale));
+        const uint32_t c = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+        w[i >> 1] |= (c & 0xFFFFu) << (16 * (i & 1));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// The angles of this lane's columns col .. col + 7 (col < rot).
+template <bool kInterleaved>
+struct Angles {
+    float c[kInterleaved ? 4 : 8], s[kInterleaved ? 4 : 8];
+    __device__ __forceinline__ void load(const float* row, int col, int rot) {
+        const int half = rot >> 1;
+        const int at = kInterleaved ? (col >> 1) : (col < half ? col : col - half);
+#pragma unroll
+        for (int j = 0; j < (kInterleaved ? 4 : 8); j += 4) {
+            *reinterpret_cast<float4*>(c + j) = __ldg(reinterpret_cast<const float4*>(row + at + j));
+            *reinterpret_cast<float4*>(s + j) = __ldg(reinterpret_cast<const float4*>(row + half + at + j));
+        }
+    }
+};
+
+// Turns this lane's 8 columns.  Half-split pairs sit in the lane `rot / 16`
+// away (all lanes of the warp take part in the exchange).
+template <bool kInterleaved>
+__device__ __forceinline__ void turn8(float (&x)[8], const Angles<kInterleaved>& a, int col, int rot, int lane) {
+    if constexpr (kInterleaved) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float u = x[2 * j], w = x[2 * j + 1];
+            x[2 * j] = __fsub_rn(__fmul_rn(u, a.c[j]), __fmul_rn(w, a.s[j]));
+            x[2 * j + 1] = __fadd_rn(__fmul_rn(w, a.c[j]), __fmul_rn(u, a.s[j]));
+        }
+    } else {
+        const bool low = col < (rot >> 1);
+        const int partner = low ? lane + rot / 16 : lane - rot / 16;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float y = __shfl_sync(0xffffffffu, x[j], partner & 31);
+            x[j] = low ? __fsub_rn(__fmul_rn(x[j], a.c[j]), __fmul_rn(y, a.s[j]))
+                       : __fadd_rn(__fmul_rn(x[j], a.c[j]), __fmul_rn(y, a.s[j]));
+        }
+    }
+}
+
+// Heads [h0, h0 + n) of one token, W columns each: read, turned (columns below
+// rot), written.  n <= kAppendRowBytes / (2 W), so all loads are in flight at once.
+template <int W>
+struct HeadRows {
+    static constexpr int kLanes = W / 8;                                      // lanes per row
+    static constexpr int kRows = 32 / kLanes;                                 // rows at a time
+    static constexpr int kSteps = kAppendRowBytes / (2 * W) / kRows;          // 4
+    static constexpr int kHeads = kRows * kSteps;
+    uint4 raw[kSteps];
+    __device__ __forceinline__ void load(const __nv_bfloat16* src, long long head_stride, int n, int lane) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int h = i * kRows + lane / kLanes;
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (h < n) raw[i] = *reinterpret_cast<const uint4*>(src + h * head_stride + (lane % kLanes) * 8);
+        }
+    }
+    template <bool kInterleaved>
+    __device__ __forceinline__ void turn(const float* angles, int rot, int lane) {
+        const int col = (lane % kLanes) * 8;
+        Angles<kInterleaved> ang;
+        if (col < rot) ang.load(angles, col, rot);
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            float x[8];
+            unpack8(raw[i], x);
+            turn8<kInterleaved>(x, ang, col, rot, lane);
+            if (col < rot) raw[i] = pack8(x);
+        }
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16* dst, long long head_stride, int n, int lane) const {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int h = i * kRows + lane / kLanes;
+            if (h < n) *reinterpret_cast<uint4*>(dst + h * head_stride + (lane % kLanes) * 8) = raw[i];
+        }
+    }
+};
+
+template <int W, bool kInterleaved>
+__device__ __forceinline__ void query_task(const AppendArgs& a, int i, int chunk, int lane) {
+    using R = HeadRows<W>;
+    const int h0 = chunk * R::kHeads;
+    const int n = a.H - h0 < R::kHeads ? a.H - h0 : R::kHeads;
+    R rows;
+    rows.load(a.q_in + i * a.qi_token + h0 * a.qi_head, a.qi_head, n, lane);
+    int b, pos;
+    place_token(a, i, lane, b, pos);
+    if (pos < 0) return;
+    rows.template turn<kInterleaved>(a.cos_sin + static_cast<long long>(pos) * a.rot, a.rot, lane);
+    rows.store(a.q_out + i * a.qo_token + h0 * a.qo_head, a.qo_head, n, lane);
+}
+
+// Latent cache: task 0 of a token is its row [latent 512 | turned k_rope 64],
+// the others 16 of its query heads' rope columns.
+template <bool kFp8, bool kInterleaved>
+__global__ void __launch_bounds__(kAppendThreads) mla_cache_append_kernel(const AppendArgs a, int tasks_per_token) {
+    const int lane = threadIdx.x & 31;
+    const long long w = (static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x) >> 5;
+    const long long token = w / tasks_per_token;
+    if (token >= a.T) return;
+    const int i = static_cast<int>(token);
+    const int task = static_cast<int>(w - token * tasks_per_token);
+    if (task > 0) {
+        query_task<64, kInterleaved>(a, i, task - 1, lane);
+        return;
+    }
+    const __nv_bfloat16* latent = a.k + i * a.k_token;
+    // bf16: columns 8 lane, 256 + 8 lane (rows of 512 bytes a step); E4M3: 16 lane .. 16 lane + 15 (16 bytes of codes)
+    const int c0 = kFp8 ? 16 * lane : 8 * lane, c1 = kFp8 ? 16 * lane + 8 : 256 + 8 * lane;
+    const uint4 r0 = *reinterpret_cast<const uint4*>(latent + c0);
+    const uint4 r1 = *reinterpret_cast<const uint4*>(latent + c1);
+    float x[8];
+    const int col = (lane & 7) * 8;
+    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+    if (lane < 8) raw = *reinterpret_cast<const uint4*>(a.v + i * a.v_token + col);
+    int b, pos;
+    place_token(a, i, lane, b, pos);
+    if (pos < 0) return;
+    const long long row = cache_row(a, b, pos, lane);
+    if (row < 0) return;
+    Angles<kInterleaved> ang;
+    ang.load(a.cos_sin + static_cast<long long>(pos) * a.rot, col, a.rot);
+    unpack8(raw, x);
+    turn8<kInterleaved>(x, ang, col, a.rot, lane);
+    if constexpr (kFp8) {
+        uint8_t* dst = static_cast<uint8_t*>(a.k_pages) + row * kDqk;
+        float y[8], z[8];
+        unpack8(r0, y);
+        unpack8(r1, z);
+        const uint2 lo = quantise8(y, a.kv_scale), hi = quantise8(z, a.kv_scale);
+        *reinterpret_cast<uint4*>(dst + c0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        if (lane < 8) *reinterpret_cast<uint2*>(dst + kDv + col) = quantise8(x, a.kv_scale);
+    } else {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.k_pages) + row * kDqk;
+        *reinterpret_cast<uint4*>(dst + c0) = r0;
+        *reinterpret_cast<uint4*>(dst + c1) = r1;
+        if (lane < 8) *reinterpret_cast<uint4*>(dst + kDv + col) = pack8(x);
+    }
+}
+
+// Keys and values of grouped kv heads, 128 wide: a token's tasks are its key
+// heads (turned), its value heads (copied) and its query heads, 8 at a time.
+template <bool kInterleaved>
+__global__ void __launch_bounds__(kAppendThreads) mha_cache_append_kernel(const AppendArgs a, int tasks_per_token) {
+    using R = HeadRows<128>;
+    const int lane = threadIdx.x & 31;
+    const long long w = (static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x) >> 5;
+    const long long token = w / tasks_per_token;
+    if (token >= a.T) return;
+    const int i = static_cast<int>(token);
+    int task = static_cast<int>(w - token * tasks_per_token);
+    const int kv_tasks = (a.Hkv + R::kHeads - 1) / R::kHeads;
+    if (task >= 2 * kv_tasks) {
+        query_task<128, kInterleaved>(a, i, task - 2 * kv_tasks, lane);
+        return;
+    }
+    const bool value = task >= kv_tasks;
+    if (value) task -= kv_tasks;
+    const int h0 = task * R::kHeads;
+    const int n = a.Hkv - h0 < R::kHeads ? a.Hkv - h0 : R::kHeads;
+    R rows;
+    rows.load(value ? a.v + i * a.v_token + h0 * a.v_head : a.k + i * a.k_token + h0 * a.k_head,
+              value ? a.v_head : a.k_head, n, lane);
+    int b, pos;
+    place_token(a, i, lane, b, pos);
+    if (pos < 0) return;
+    const long long row = cache_row(a, b, pos, lane);
+    if (row < 0) return;
+    if (!value) rows.template turn<kInterleaved>(a.cos_sin + static_cast<long long>(pos) * a.rot, a.rot, lane);
+    __nv_bfloat16* pages = value ? a.v_pages : static_cast<__nv_bfloat16*>(a.k_pages);
+    rows.store(pages + (row * a.Hkv + h0) * 128, 128, n, lane);
+}
+
+}  // namespace mla

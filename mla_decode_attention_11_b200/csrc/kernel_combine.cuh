@@ -15,6 +15,7 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "paged.cuh"
 #include "ptx.cuh"
 #include "schedule.cuh"
 
@@ -56,9 +57,11 @@ inline int combine_grid_y(int B, int R, int num_sms) {
 }
 
 // DV: value width (512 for MLA, 128 for MHA); a lane owns DV / 128 float4 columns.
-template <int DV = kDv>
+// CV: where the lengths come from (paged.cuh); in a paged run a row may have
+// seen no key of any piece: it gets out = 0 and lse = -inf (or its sink).
+template <int DV = kDv, class CV = ContigKv>
 __global__ void __launch_bounds__(kCombineThreads, 2)
-    mla_decode_combine_kernel(const CombineArgs args) {
+    mla_decode_combine_kernel(const CombineArgs args, const __grid_constant__ typename CV::Args pa) {
     static_assert(DV == 512 || DV == 128, "value width");
     constexpr int NV4 = DV / 128;  // float4 columns per lane
     __shared__ int s_split;
@@ -70,7 +73,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
     // the schedule the main kernel used for these lengths, its unit count and
     // the flat unit offset of sequence b (units: tiles, or S-tile chunks)
     if (warp == 0) {
-        const ScheduleScan sc = schedule_scan_warp(args.seqlens, args.B, args.L_max, args.P, args.split_tiles, b);
+        const ScheduleScan sc = schedule_scan_warp(make_lens(args, pa), args.B, args.P, args.split_tiles, b);
         if (lane == 0) {
             s_split = sc.S;
             s_acc = sc.acc_at;
@@ -86,7 +89,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
     const int rows_per = (args.R + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
     const int r_lo = static_cast<int>(blockIdx.y) * rows_per;
     const int r_hi = r_lo + rows_per < args.R ? r_lo + rows_per : args.R;
-    const int L = clamp_len(__ldg(args.seqlens + b), args.L_max, nullptr);
+    const int L = make_lens(args, pa)(b);
     const long long n = num_units(L, S);
     if (n == 0) {
         for (int r = r_lo + warp; r < r_hi; r += kCombineWarps) {
@@ -143,6 +146,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         m = fmaxf(m, sink);
+        if (CV::kPaged && m == -INFINITY) m = 0.f;
         const float my_e = lane < k ? expf(my_l - m) : 0.f;
         float sum = my_e;
         for (int i = lane + 32; i < k; i += 32) sum += expf(args.part_lse[prow_of(i)] - m);
@@ -150,7 +154,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         sum += expf(sink - m);
         const float lse_all = m + logf(sum);
-        const float inv = 1.f / sum;
+        const float inv = (CV::kPaged && sum == 0.f) ? 0.f : 1.f / sum;
         const float my_w = my_e * inv;  // weight of piece `lane`: exp(lse_lane - lse)
 
         // out = sum_i exp(lse_i - lse) * (O_i / l_i); lane owns float4 columns lane + 32 v
@@ -187,6 +191,152 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
             *reinterpret_cast<uint2*>(dst + e0 / 2) = pk;
         }
         if (lane == 0) args.lse[orow] = lse_all;
+    }
+}
+
+// Shared prefix.  A row's keys are the prefix's (pieces of the 128-row group
+// that holds the row, rows of all sequences end to end) and its sequence's own;
+// every piece of either left a partial, and this merges them.  Pieces of a
+// group and of a sequence are found as the main kernels' schedules cut them.
+struct PrefixCombineArgs {
+    int B, R, H;
+    int P_own, P_pre;           // partitions of the two main launches
+    int groups;                 // 128-row groups, the last one perhaps not full
+    __nv_bfloat16* out;
+    float* lse;
+    const float* own_o;         // [2 P_own + B, R, 512]
+    const float* own_lse;
+    const float* pre_o;         // [2 P_pre + groups, 128, 512]
+    const float* pre_lse;
+    const float* sinks;
+};
+
+__global__ void __launch_bounds__(kCombineThreads, 2)
+    mla_prefix_combine_kernel(const PrefixCombineArgs args, const __grid_constant__ PagedArgs own,
+                              const __grid_constant__ PagedArgs pre) {
+    constexpr int NV4 = kDv / 128;
+    __shared__ int s_split;
+    __shared__ long long s_acc, s_tot;
+    const int b = blockIdx.x;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (warp == 0) {
+        const ScheduleScan sc = schedule_scan_warp(PagedLens{&own}, args.B, args.P_own, 0, b);
+        if (lane == 0) {
+            s_split = sc.S;
+            s_acc = sc.acc_at;
+            s_tot = sc.units;
+        }
+    }
+    __syncthreads();
+    ptx::wait_prior_grid();
+    // this sequence's own pieces: k_own of them from slot s0 on, then every second one
+    const long long n = num_units(PagedLens{&own}(b), s_split);
+    int k_own = 0, own_p0 = 0;
+    bool own_whole = true;
+    if (n > 0) {
+        k_own = 1;
+        if (s_split == 0) {
+            const long long T = (s_tot + args.P_own - 1) / args.P_own;
+            own_p0 = static_cast<int>(s_acc / T);
+            k_own = static_cast<int>((s_acc + n - 1) / T) - own_p0 + 1;
+            own_whole = (k_own == 1);
+        }
+    }
+    // the prefix: every group has the same tiles
+    const long long n_pre = num_tiles(PagedLens{&pre}(0));
+    const bool pre_one = pick_schedule(n_pre * args.groups, n_pre, args.groups, args.P_pre) > 0;
+    const long long T_pre = n_pre > 0 ? (n_pre * args.groups + args.P_pre - 1) / args.P_pre : 1;
+
+    const int rows_per = (args.R + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
+    const int r_lo = static_cast<int>(blockIdx.y) * rows_per;
+    const int r_hi = r_lo + rows_per < args.R ? r_lo + rows_per : args.R;
+    for (int r = r_lo + warp; r < r_hi; r += kCombineWarps) {
+        const long long orow = static_cast<long long>(b) * args.R + r;
+        const long long grp = orow >> 7;
+        int k_pre = 0, pre_p0 = 0;
+        bool pre_whole = true;
+        if (n_pre > 0) {
+            k_pre = 1;
+            if (!pre_one) {
+                pre_p0 = static_cast<int>(grp * n_pre / T_pre);
+                k_pre = static_cast<int>((grp * n_pre + n_pre - 1) / T_pre) - pre_p0 + 1;
+                pre_whole = (k_pre == 1);
+            }
+        }
+        const int k = k_own + k_pre;
+        const float sink = args.sinks ? args.sinks[r % args.H] : -INFINITY;
+        // partial row of piece i: the sequence's pieces, then the group's
+        auto prow_of = [&](int i) -> size_t {
+            if (i < k_own) {
+                const long long s = own_whole ? 2LL * args.P_own + b : (i == 0 ? 2 * own_p0 + 1 : 2 * (own_p0 + i));
+                return static_cast<size_t>(s * args.R + r);
+            }
+            const int j = i - k_own;
+            const long long s = pre_whole ? 2LL * args.P_pre + grp : (j == 0 ? 2 * pre_p0 + 1 : 2 * (pre_p0 + j));
+            return static_cast<size_t>(s * 128 + (orow & 127));
+        };
+        auto lse_of = [&](int i) { return (i < k_own ? args.own_lse : args.pre_lse)[prow_of(i)]; };
+        float4 x[4][NV4];
+        auto load_batch = [&](int i0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (i0 + j < k) {
+                    const float4* src = reinterpret_cast<const float4*>(
+                        (i0 + j < k_own ? args.own_o : args.pre_o) + prow_of(i0 + j) * kDv);
+#pragma unroll
+                    for (int v = 0; v < NV4; ++v) x[j][v] = __ldcs(src + lane + 32 * v);
+                }
+            }
+        };
+        load_batch(0);
+        const float my_l = lane < k ? lse_of(lane) : -INFINITY;
+        float m = my_l;
+        for (int i = lane + 32; i < k; i += 32) m = fmaxf(m, lse_of(i));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m = fmaxf(m, sink);
+        if (m == -INFINITY) m = 0.f;  // nothing to see and no sink: out = 0, lse = -inf
+        const float my_e = lane < k ? expf(my_l - m) : 0.f;
+        float sum = my_e;
+        for (int i = lane + 32; i < k; i += 32) sum += expf(lse_of(i) - m);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sum += expf(sink - m);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float my_w = my_e * inv;
+        float4 acc_o[NV4];
+#pragma unroll
+        for (int v = 0; v < NV4; ++v) acc_o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = 0; i0 < k; i0 += 4) {
+            if (i0 > 0) load_batch(i0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = i0 + j;
+                if (i < k) {
+                    const float w = i < 32 ? __shfl_sync(0xffffffffu, my_w, i) : expf(lse_of(i) - m) * inv;
+#pragma unroll
+                    for (int v = 0; v < NV4; ++v) {
+                        acc_o[v].x += w * x[j][v].x;
+                        acc_o[v].y += w * x[j][v].y;
+                        acc_o[v].z += w * x[j][v].z;
+                        acc_o[v].w += w * x[j][v].w;
+                    }
+                }
+            }
+        }
+        __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(args.out + orow * kDv);
+#pragma unroll
+        for (int v = 0; v < NV4; ++v) {
+            const int e0 = (lane + 32 * v) * 4;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc_o[v].x, acc_o[v].y);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc_o[v].z, acc_o[v].w);
+            uint2 pk;
+            pk.x = *reinterpret_cast<const uint32_t*>(&lo);
+            pk.y = *reinterpret_cast<const uint32_t*>(&hi);
+            *reinterpret_cast<uint2*>(dst + e0 / 2) = pk;
+        }
+        if (lane == 0) args.lse[orow] = m + logf(sum);
     }
 }
 

@@ -134,10 +134,15 @@ __device__ __forceinline__ int q_row_exponent(float amax) {
 }
 
 
-template <int G>
+// CV: where the cache's rows are (paged.cuh).  In pages, tm_kv's outer
+// dimensions are (row of a page, page) and a chunk is 128 / box boxes stacked in
+// the same layout, each issued by its own lane of the producer warp.
+template <int G, class CV = ContigKv>
 __global__ void __launch_bounds__(192, 1)
-    mla_decode_fp8mma_kernel(const __grid_constant__ CUtensorMap tm_kv, const MainArgs args) {
+    mla_decode_fp8mma_kernel(const __grid_constant__ CUtensorMap tm_kv, const MainArgs args,
+                             const __grid_constant__ typename CV::Args pa) {
     using C = Fp8MmaCfg<G>;
+    using Walker = PieceWalkerOf<typename CV::Lens>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 
@@ -201,12 +206,12 @@ __global__ void __launch_bounds__(192, 1)
         ptx::tmem_relinquish();
     }
     if (warp == 0) {
-        const ScheduleScan sc = schedule_scan_warp(args.seqlens, args.B, args.L_max, args.P, args.split_tiles);
+        const ScheduleScan sc = schedule_scan_warp(make_lens(args, pa), args.B, args.P, args.split_tiles);
         const long long total = sc.units;
         const long long T = (total + args.P - 1) / args.P;
         int bf;
         long long af;
-        locate_warp(args.seqlens, args.B, args.L_max, sc.S, static_cast<long long>(p) * T, &bf, &af);
+        locate_warp(make_lens(args, pa), args.B, sc.S, static_cast<long long>(p) * T, &bf, &af);
         if (lane == 0) {
             *b_first_slot = bf;
             *acc_first_slot = af;
@@ -225,13 +230,12 @@ __global__ void __launch_bounds__(192, 1)
     // dependent) may start scheduling its CTAs; it waits for this grid's results
     ptx::launch_dependents();
 
-    PieceWalker walker;
+    Walker walker;
     {
         const long long total = *total_slot;
         const long long T = (total + args.P - 1) / args.P;
-        walker.seqlens = args.seqlens;
+        walker.lens = make_lens(args, pa);
         walker.B = args.B;
-        walker.L_max = args.L_max;
         walker.p = p;
         walker.S = *split_slot;
         walker.k = 0;
@@ -244,13 +248,80 @@ __global__ void __launch_bounds__(192, 1)
 
     if (warp == 4) {
         // ============================================================ TMA producer
-        if (ptx::elect_one()) {
+        if constexpr (CV::kPaged) {
+            // the whole warp walks; lane l issues box l of each chunk
+            uint32_t pair_cnt = 0, rope_cnt = 0;
+            int unit = 0;
+            bool ok = true;
+            const bool issues = lane < (kTileKV >> pa.box_log2);
+            const uint32_t dst_off = static_cast<uint32_t>(lane << pa.box_log2) * kChunk;  // a box row is 64 bytes
+            BoxStream<Walker> boxes(pa, walker, issues ? lane << pa.box_log2 : kTileKV);
+            Box ahead = boxes.next();  // the tile prefetched into L2 while the one before it is loaded
+            Box late = boxes.next();   // and the one whose table entry is on its way
+            Piece pc;
+            while (ok && walker.next(pc)) {
+                for (int t = pc.tile_lo; t < pc.tile_hi && ok; ++t) {
+                    const Box box = ahead;
+                    ahead = late;
+                    late = boxes.next();
+                    if (args.prefetch_tiles > 0 && issues && ahead.some && ahead.page >= 0 &&
+                        ahead.page < pa.num_pages)
+                        for (int j = 0; j < kNumChunks; ++j)
+                            ptx::tma_prefetch_3d(&tm_kv, j * kChunk, ahead.row, ahead.page);
+                    const int page = issues ? usable(pa, box, args.status) : 0;
+                    auto arm = [&](uint64_t* full, uint64_t* empty, uint32_t cnt, uint32_t slots, uint32_t bytes) {
+                        ok = ptx::mbar_wait_bounded(empty, ((cnt / slots) & 1) ^ 1, tmo);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) return false;
+                        if (lane == 0) ptx::mbar_arrive_expect_tx(full, bytes);
+                        __syncwarp();
+                        return issues && !(blockIdx.x == 0 && unit == args.stall_unit);
+                    };
+                    {
+                        const uint32_t s = rope_cnt % C::NR;
+                        if (arm(rope_full + s, rope_empty + s, rope_cnt, C::NR, C::kChunkBytes))
+                            ptx::tma_load_3d(rope_smem + s * C::kChunkBytes + dst_off, &tm_kv, rope_full + s,
+                                             (kNumChunks - 1) * kChunk, box.row, page);
+                        if (!ok) break;
+                        ++unit;
+                        ++rope_cnt;
+                    }
+                    for (int pp = 0; pp < 4; ++pp) {
+                        const uint32_t s = pair_cnt % C::NP;
+                        if (arm(pair_full + s, pair_empty + s, pair_cnt, C::NP, C::kPairBytes)) {
+                            uint8_t* dst = pair_smem + s * C::kPairBytes + dst_off;
+                            ptx::tma_load_3d(dst, &tm_kv, pair_full + s, (2 * pp) * kChunk, box.row, page);
+                            ptx::tma_load_3d(dst + C::kChunkBytes, &tm_kv, pair_full + s, (2 * pp + 1) * kChunk,
+                                             box.row, page);
+                        }
+                        if (!ok) break;
+                        ++unit;
+                        ++pair_cnt;
+                    }
+                }
+            }
+            if (!ok && lane == 0) {
+                atomicOr(args.status, kStatusTimeout);
+                *abort_flag = 1;
+            }
+            // drain: every armed load must land before the CTA exits (bounded)
+            if (lane == 0) {
+                for (uint32_t i = 0; i < C::NP && i < pair_cnt; ++i) {
+                    const uint32_t use = pair_cnt - 1 - i;
+                    ptx::mbar_wait_bounded(pair_full + (use % C::NP), (use / C::NP) & 1, tmo);
+                }
+                for (uint32_t i = 0; i < C::NR && i < rope_cnt; ++i) {
+                    const uint32_t use = rope_cnt - 1 - i;
+                    ptx::mbar_wait_bounded(rope_full + (use % C::NR), (use / C::NR) & 1, tmo);
+                }
+            }
+        } else if (ptx::elect_one()) {
             uint32_t pair_cnt = 0, rope_cnt = 0;
             int unit = 0;
             bool ok = true;
             // L2 prefetch cursor `prefetch_tiles` tiles ahead of the loads,
             // across piece boundaries (a tile's 9 chunk boxes)
-            PieceWalker pf_walker = walker;
+            Walker pf_walker = walker;
             Piece pf_pc{};
             bool pf_live = false, pf_started = false;
             int pf_t = 0;
@@ -523,6 +594,8 @@ __global__ void __launch_bounds__(192, 1)
             ok = ptx::mbar_wait_bounded(q_ready, piece_cnt & 1, tmo);  // every row's scale is in qscale
             if (!ok) break;
 
+            SeqView view{};
+            if constexpr (CV::kPaged) view = view_of(pa, paged_len(pa, pc.b));
             float m_ref[G];
             float l_part[G];
 #pragma unroll
@@ -533,9 +606,9 @@ __global__ void __launch_bounds__(192, 1)
             for (int t = pc.tile_lo; t < pc.tile_hi; ++t) {
                 const bool first = (t == pc.tile_lo);
                 int row0 = t * kTileKV;
-                if (row0 + kTileKV > pc.L) row0 = pc.L - kTileKV;
+                if (!CV::kPaged && row0 + kTileKV > pc.L) row0 = pc.L - kTileKV;
                 const int kv_row = row0 + row_in_tile;
-                const bool valid = (kv_row >= t * kTileKV) && (kv_row < pc.L);
+                const bool valid = CV::kPaged || ((kv_row >= t * kTileKV) && (kv_row < pc.L));
 
                 const uint32_t sb = tile_cnt & 1;  // S^T and P buffer of this tile
                 ok = ptx::mbar_wait_bounded(s_full + sb, (tile_cnt >> 1) & 1, tmo);
@@ -561,6 +634,7 @@ __global__ void __launch_bounds__(192, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) x[c0 + j] = valid ? acc[j] * qscale[c0 + j] : -INFINITY;
                 }
+                if constexpr (CV::kPaged) mask_columns<G>(pa, view, x, row0, kv_row, g * G, args.H, args.Sq - 1);
                 // column max over the tile's 128 kv rows
                 float* redmax = red + (tile_cnt & 1) * 4 * G;
                 const float wmax = warp_reduce_scatter<G, true>(x, lane);
@@ -596,7 +670,8 @@ __global__ void __launch_bounds__(192, 1)
 #pragma unroll
                     for (int j = 0; j < G; ++j) {
                         const float mn = fmaxf(m_ref[j], tmax[j]);
-                        alpha[j] = ex2_approx(m_ref[j] - mn);
+                        // paged: a column that has seen no key yet (both -inf) stays as it is
+                        alpha[j] = (CV::kPaged && m_ref[j] == mn) ? 1.f : ex2_approx(m_ref[j] - mn);
                         m_ref[j] = mn;
                         l_part[j] *= alpha[j];
                     }
@@ -623,14 +698,18 @@ __global__ void __launch_bounds__(192, 1)
                 uint32_t w1[G / 4], w2[G / 4];
 #pragma unroll
                 for (int j = 0; j < G; j += 2) {
-                    const float p0 = ex2_approx(x[j] - m_ref[j] + C::kPScaleLog2);
-                    const float p1 = ex2_approx(x[j + 1] - m_ref[j + 1] + C::kPScaleLog2);
+                    const float m0 = (CV::kPaged && m_ref[j] == -INFINITY) ? 0.f : m_ref[j];
+                    const float m1 = (CV::kPaged && m_ref[j + 1] == -INFINITY) ? 0.f : m_ref[j + 1];
+                    const float p0 = ex2_approx(x[j] - m0 + C::kPScaleLog2);
+                    const float p1 = ex2_approx(x[j + 1] - m1 + C::kPScaleLog2);
                     const uint32_t t1 = f32x2_to_e4m3x2(p0, p1);
                     const float2 v1 = e4m3x2_to_f32x2(t1);
                     const uint32_t t2 = f32x2_to_e4m3x2(p0 - v1.x, p1 - v1.y);
                     const float2 v2 = e4m3x2_to_f32x2(t2);
-                    l_part[j] += v1.x + v2.x;  // the weights the MMAs use
-                    l_part[j + 1] += v1.y + v2.y;
+                    // the weights the MMAs use; in pages the weights before their rounding, so
+                    // that the lse of a few keys is as exact as its scores are
+                    l_part[j] += CV::kPaged ? p0 : v1.x + v2.x;
+                    l_part[j + 1] += CV::kPaged ? p1 : v1.y + v2.y;
                     if ((j & 2) == 0) {
                         w1[j / 4] = t1;
                         w2[j / 4] = t2;
@@ -645,6 +724,19 @@ __global__ void __launch_bounds__(192, 1)
                         make_uint4(w1[4 * u], w1[4 * u + 1], w1[4 * u + 2], w1[4 * u + 3]);
                     *reinterpret_cast<uint4*>(p_buf + swz_offset(row_in_tile, kUnitsPerTerm + u, C::NO)) =
                         make_uint4(w2[4 * u], w2[4 * u + 1], w2[4 * u + 2], w2[4 * u + 3]);
+                }
+                if constexpr (CV::kPaged) {
+                    // values of rows that no token sees: P is 0 there, and 0 times
+                    // whatever the page holds (a NaN code) must be 0
+                    if (tile_unseen(pa, view, t) && unseen(pa, view, kv_row)) {
+#pragma unroll 1
+                        for (uint32_t pp = 0; pp < 4; ++pp) {
+                            uint8_t* vrow =
+                                pair_smem + ((4 * tile_cnt + pp) % C::NP) * C::kPairBytes + row_in_tile * kChunk;
+                            clear_row<kChunk>(vrow, lane);
+                            clear_row<kChunk>(vrow + C::kChunkBytes, lane);
+                        }
+                    }
                 }
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_before();
@@ -676,8 +768,11 @@ __global__ void __launch_bounds__(192, 1)
                 float lj = (redsum[0 * G + j] + redsum[1 * G + j] + redsum[2 * G + j] + redsum[3 * G + j]) *
                            C::kPScaleInv;
                 float c = 1.f;
-                if (sink_here) c = fold_sink(mj, lj, args.sinks[qr % args.H] * kLog2e);
-                fin[j] = c / lj * args.o_scale * C::kPScaleInv;
+                if (sink_here) {
+                    const float s2 = args.sinks[qr % args.H] * kLog2e;
+                    c = CV::kPaged ? fold_sink_any(mj, lj, s2) : fold_sink(mj, lj, s2);
+                }
+                fin[j] = (CV::kPaged && lj == 0.f) ? 0.f : c / lj * args.o_scale * C::kPScaleInv;
                 const float lse_nat = (mj + log2f(lj)) * 0.69314718055994530942f;
                 if (pc.slot < 0)
                     args.lse[static_cast<size_t>(pc.b) * args.R + qr] = lse_nat;

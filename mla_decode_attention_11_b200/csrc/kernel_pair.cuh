@@ -47,6 +47,14 @@
 // than a release arrive.  Loads of both CTAs are counted on the leader's
 // barriers (2-SM TMA); MMA completion is multicast to both CTAs.
 // Every wait is bounded; on expiry a CTA records kStatusTimeout and unwinds.
+//
+// The cache in pages (CV = PagedKv, paged.cuh).  The producers' warps walk
+// whole: lane l issues the l-th box of a K chunk (64 / box of them) or V slot
+// (128 / box).  A V slot is then [128 / box][2 chunks][box rows][128 bytes],
+// as its boxes land; each 16-row step of the PV MMAs lies in one box, so only
+// the descriptors' offsets differ.  In a tile with rows that no token sees, the
+// softmax threads clear those rows of V: the PV issuer waits for the tile's V
+// slots first and tells both CTAs (v_here), the follower by st.async.
 #pragma once
 
 #include <cuda.h>
@@ -54,6 +62,7 @@
 #include <cstdint>
 
 #include "kernel_transposed.cuh"
+#include "paged.cuh"
 #include "ptx.cuh"
 #include "schedule.cuh"
 
@@ -79,25 +88,28 @@ struct PairCfg {
     static constexpr int OFF_BAR = OFF_RED + 384 * 4;
     // q_full, q_empty, pv_done[NP], drain_s, drain_pv, group_sync, s_full[NS], p_full[NS], p_local[NS],
     // k_full[NK], k_empty[NK], v_full[NV], v_empty[NV]
-    static constexpr int kNumBars = 6 + NP + 3 * NS + 2 * NK + 2 * NV;
+    // and v_here: paged, the V slots of a tile with rows to clear have landed
+    static constexpr int kNumBars = 7 + NP + 3 * NS + 2 * NK + 2 * NV;
     static constexpr int OFF_MISC = OFF_BAR + kNumBars * 8;
     static constexpr int kSmemBytes = OFF_MISC + 64;
     static constexpr uint32_t kTmemCols = 512;                 // O: [0,256), S buffers from 256, 64 each
     static constexpr uint32_t kColS = 256;
     static_assert(NS >= 2 && 256 + 64 * NS <= 512, "S buffers must fit next to O in TMEM");
-    static_assert(NS <= 4, "one 4-byte forwarding slot per S buffer in the 64-byte misc area (words 12..15)");
+    static_assert(NS <= 3, "one 4-byte forwarding slot per S buffer and one for v_here in the 64-byte misc area (words 12..15)");
     static constexpr uint32_t kIdescS = ptx::make_idesc_bf16(128, 128, 0, 0);
     static constexpr uint32_t kIdescPV = ptx::make_idesc_bf16(128, 256, 0, 1);
     static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
-template <int NK, int NV, int NS, int NP>
+template <int NK, int NV, int NS, int NP, class CV = ContigKv>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     mla_decode_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_pf,
                            const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_part,
-                           const MainArgs args) {
+                           const MainArgs args, const __grid_constant__ typename CV::Args pa) {
     using C = PairCfg<NK, NV, NS, NP>;
+    using Walker = PieceWalkerOf<typename CV::Lens>;
+    static_assert(!CV::kPaged || NV == 2, "the V slots of a whole tile are resident while its unseen rows are cleared");
     extern __shared__ __align__(1024) uint8_t smem[];
 
     uint8_t* q_smem = smem + C::OFF_Q;
@@ -121,6 +133,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     uint64_t* k_empty = k_full + NK;
     uint64_t* v_full = k_empty + NK;
     uint64_t* v_empty = v_full + NV;
+    uint64_t* v_here = v_empty + NV;        // paged: this CTA's V slots of a tile with rows to clear have landed
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     uint32_t* tmem_base_slot = misc + 0;
     int* b_first_slot = reinterpret_cast<int*>(misc + 2);
@@ -161,6 +174,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             ptx::mbar_init(v_full + i, 1);
             ptx::mbar_init(v_empty + i, 1);
         }
+        ptx::mbar_init(v_here, 1);
         ptx::fence_mbarrier_init();
         if (!smem_ok) atomicOr(args.status, kStatusTimeout);
     }
@@ -169,21 +183,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         ptx::tmem_relinquish_pair();
     }
     if (warp == 0) {
-        const ScheduleScan sc = schedule_scan_warp(args.seqlens, args.B, args.L_max, args.P, args.split_tiles);
+        const ScheduleScan sc = schedule_scan_warp(make_lens(args, pa), args.B, args.P, args.split_tiles);
         const int S_eff = sc.S;
         const long long total = sc.units;
         const long long T = (total + args.P - 1) / args.P;
         int bf;
         long long af;
-        locate_warp(args.seqlens, args.B, args.L_max, S_eff, static_cast<long long>(p) * T, &bf, &af);
+        locate_warp(make_lens(args, pa), args.B, S_eff, static_cast<long long>(p) * T, &bf, &af);
         if (lane == 0) {
             *b_first_slot = bf;
             *acc_first_slot = af;
             *total_slot = total;
             *split_slot = S_eff;
         }
-        if (blockIdx.x == 0)
-            for (int b = lane; b < args.B; b += 32) clamp_len(args.seqlens[b], args.L_max, args.status);
+        if (blockIdx.x == 0) {
+            int n = args.B;
+            if constexpr (CV::kPaged) n = pa.len_stride ? n : 1;
+            for (int b = lane; b < n; b += 32) clamp_len(args.seqlens[b], args.L_max, args.status);
+        }
     }
     if (warp == 4 && lane == 0) {
         ptx::prefetch_tmap(&tm_q);
@@ -202,13 +219,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     // dependent) may start scheduling its CTAs; it waits for this grid's results
     ptx::launch_dependents();
 
-    PieceWalker walker;
+    Walker walker;
     {
         const long long total = *total_slot;
         const long long T = (total + args.P - 1) / args.P;
-        walker.seqlens = args.seqlens;
+        walker.lens = make_lens(args, pa);
         walker.B = args.B;
-        walker.L_max = args.L_max;
         walker.p = p;
         walker.S = *split_slot;
         walker.k = 0;
@@ -220,10 +236,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     // shared::cluster addresses of the leader's barriers
     const uint32_t lead_q_full = ptx::mapa_shared(ptx::smem_u32(q_full), 0);
     const bool stall_cta = (blockIdx.x == 0);
+    uint32_t box_rows = kTileKV;
+    if constexpr (CV::kPaged) box_rows = static_cast<uint32_t>(pa.box);
 
     if (warp == 4) {
         // ============================================================ Q + K producer
-        if (ptx::elect_one()) {
+        if constexpr (CV::kPaged) {
+            uint32_t k_cnt = 0, piece_cnt = 0;
+            int unit = 0;
+            bool ok = true;
+            const bool issues = lane < (64 >> pa.box_log2);  // the boxes of this CTA's 64 rows of a tile
+            const int off = lane << pa.box_log2;
+            BoxStream<Walker> boxes(pa, walker, issues ? static_cast<int>(rank) * 64 + off : kTileKV);
+            Box cur = boxes.next(), ahead = cur;  // the tile loaded, the tile prefetched into L2
+            Box late = boxes.next();              // and the one whose table entry is on its way
+            Piece pc;
+            bool started = false;
+            while (ok && walker.next(pc)) {
+                if (piece_cnt > 0) ok = ptx::mbar_wait_bounded(q_empty, (piece_cnt - 1) & 1, tmo);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    if (leader) ptx::mbar_arrive_expect_tx(q_full, 2 * kNumChunks * C::kQChunk);
+                    const int qrow = pc.b * args.R + g * 128 + static_cast<int>(rank) * 64;
+                    if (!(stall_cta && unit == args.stall_unit))
+                        ptx::tma_load_3d_pair(q_smem, &tm_q, lead_q_full, 0, qrow, 0);
+                }
+                ++unit;
+                for (int t = pc.tile_lo; t < pc.tile_hi && ok; ++t) {
+                    if (started) cur = ahead;
+                    started = true;
+                    ahead = late;
+                    late = boxes.next();
+                    if (args.prefetch_tiles > 0 && issues && ahead.some && ahead.page >= 0 && ahead.page < pa.num_pages)
+                        ptx::tma_prefetch_4d(&tm_pf, 0, ahead.row, 0, ahead.page);
+                    const int page = issues ? usable(pa, cur, args.status) : 0;
+                    for (int jj = 0; jj < kNumChunks; ++jj) {
+                        const int j = (jj == 0) ? 8 : jj - 1;  // rope chunk first
+                        const uint32_t s = k_cnt % NK;
+                        ok = ptx::mbar_wait_bounded(k_empty + s, ((k_cnt / NK) & 1) ^ 1, tmo);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        if (leader && lane == 0) ptx::mbar_arrive_expect_tx(k_full + s, 2 * C::kKChunk);
+                        __syncwarp();
+                        if (issues && !(stall_cta && unit == args.stall_unit))
+                            ptx::tma_load_3d_pair(k_smem + s * C::kKChunk + off * 128, &tm_k,
+                                                  ptx::mapa_shared(ptx::smem_u32(k_full + s), 0), j * kChunk, cur.row,
+                                                  page);
+                        ++unit;
+                        ++k_cnt;
+                    }
+                }
+                ++piece_cnt;
+            }
+            if (lane == 0) {
+                if (!ok) atomicOr(args.status, kStatusTimeout);
+                if (leader) {  // every armed load has landed before teardown
+                    bool drained = true;
+                    const uint32_t n_k = k_cnt < static_cast<uint32_t>(NK) ? k_cnt : static_cast<uint32_t>(NK);
+                    for (uint32_t i = 0; i < n_k; ++i) {
+                        const uint32_t c = k_cnt - 1 - i;
+                        drained &= ptx::mbar_wait_bounded(k_full + c % NK, (c / NK) & 1, tmo);
+                    }
+                    if (piece_cnt > 0) drained &= ptx::mbar_wait_bounded(q_full, (piece_cnt - 1) & 1, tmo);
+                    if (!drained) atomicOr(args.status, kStatusTimeout);
+                }
+            }
+        } else if (ptx::elect_one()) {
             // Each TMA instruction costs the issuing thread a few hundred cycles,
             // so Q (one box of all 9 chunks) and the prefetches are as large as
             // the views of q and kv with the chunk index as an outer dimension
@@ -239,7 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             // cursor starts after the first piece's Q load is out and skips the
             // first tile (loaded at once), so nothing queues ahead of the loads
             // the first MMA needs.
-            PieceWalker pf_walker = walker;
+            Walker pf_walker = walker;
             Piece pf_pc{};
             bool pf_live = false, pf_started = false;
             int pf_t = 0;
@@ -312,7 +391,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         __syncwarp();
     } else if (warp == 5) {
         // ============================================================ V producer
-        if (ptx::elect_one()) {
+        if constexpr (CV::kPaged) {
+            uint32_t v_cnt = 0;
+            bool ok = true;
+            const bool issues = lane < (kTileKV >> pa.box_log2);
+            const int off = lane << pa.box_log2;
+            BoxStream<Walker> boxes(pa, walker, issues ? off : kTileKV);
+            Box ahead = boxes.next();
+            Piece pc;
+            while (ok && walker.next(pc)) {
+                for (int t = pc.tile_lo; t < pc.tile_hi && ok; ++t) {
+                    const Box cur = ahead;
+                    ahead = boxes.next();
+                    const int page = issues ? usable(pa, cur, args.status) : 0;
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t s = v_cnt % NV;
+                        ok = ptx::mbar_wait_bounded(v_empty + s, ((v_cnt / NV) & 1) ^ 1, tmo);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        if (leader && lane == 0) ptx::mbar_arrive_expect_tx(v_full + s, 2 * C::kVSlot);
+                        __syncwarp();
+                        const int col0 = 256 * i + 128 * static_cast<int>(rank);  // two adjacent chunks, one box
+                        if (issues)
+                            ptx::tma_load_4d_pair(v_smem + s * C::kVSlot + off * 256, &tm_v,
+                                                  ptx::mapa_shared(ptx::smem_u32(v_full + s), 0), 0, cur.row,
+                                                  col0 / kChunk, page);
+                        ++v_cnt;
+                    }
+                }
+            }
+            if (lane == 0) {
+                if (!ok) atomicOr(args.status, kStatusTimeout);
+                if (leader) {
+                    bool drained = true;
+                    const uint32_t n_v = v_cnt < static_cast<uint32_t>(NV) ? v_cnt : static_cast<uint32_t>(NV);
+                    for (uint32_t i = 0; i < n_v; ++i) {
+                        const uint32_t c = v_cnt - 1 - i;
+                        drained &= ptx::mbar_wait_bounded(v_full + c % NV, (c / NV) & 1, tmo);
+                    }
+                    if (!drained) atomicOr(args.status, kStatusTimeout);
+                }
+            }
+        } else if (ptx::elect_one()) {
             uint32_t v_cnt = 0;
             bool ok = true;
             Piece pc;
@@ -427,14 +547,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             bool ok = true;
             constexpr uint16_t kBoth = 0x3;
             const uint64_t dp0 = ptx::make_smem_desc(ptx::smem_u32(p_smem), 16, 1024, ptx::Swizzle::B128);
-            const uint64_t dv0 = ptx::make_smem_desc(ptx::smem_u32(v_smem), C::kVChunk, 1024, ptx::Swizzle::B128);
+            // the next 64 value columns are one chunk of the slot (paged: of a box) further
+            const uint32_t v_chunk = CV::kPaged ? 128u * box_rows : static_cast<uint32_t>(C::kVChunk);
+            const uint64_t dv0 = ptx::make_smem_desc(ptx::smem_u32(v_smem), v_chunk, 1024, ptx::Swizzle::B128);
             uint32_t vs = 0, vph = 0;  // V ring slot and phase
             uint32_t u = 0;            // global tile index
             Piece pc;
             while (ok && walker.next(pc)) {
+                SeqView view{};
+                if constexpr (CV::kPaged) view = view_of(pa, paged_len(pa, pc.b));
                 for (int t = pc.tile_lo; ok && t < pc.tile_hi; ++t) {
                     const bool first = (t == pc.tile_lo);  // O starts over for a new piece
                     const uint32_t pb = (NP == 2) ? (u & 1) : 0;
+                    if constexpr (CV::kPaged) {
+                        if (tile_unseen(pa, view, t)) {
+                            // both of the tile's V slots are here (the loads of both CTAs are counted on
+                            // these barriers): the softmax threads may clear rows in them
+                            ok = ptx::mbar_wait_bounded_cluster(v_full, vph, tmo) &&
+                                 ptx::mbar_wait_bounded_cluster(v_full + 1, vph, tmo);
+                            if (!ok) break;
+                            ptx::mbar_arrive(v_here);
+                            ptx::st_async_u32(ptx::mapa_shared(ptx::smem_u32(fwd_slot + NS), 1), u,
+                                              ptx::mapa_shared(ptx::smem_u32(v_here), 1));
+                        }
+                    }
                     ok = ptx::mbar_wait_bounded_cluster(p_full + (u % NS), (u / NS) & 1, tmo);
                     if (!ok) break;
                     ptx::tc_fence_after();
@@ -447,7 +583,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
 #pragma unroll
                         for (int kk = 0; kk < kTileKV / 16; ++kk) {
                             const uint64_t da = dpb + (((kk >> 2) * C::kPChunk + (kk & 3) * 32) >> 4);
-                            ptx::mma_bf16_ss_pair(tmem_base + 128 * i, da, db + ((kk * 2048) >> 4), C::kIdescPV,
+                            uint32_t voff = kk * 2048;  // 16 rows of 128 bytes a step
+                            if constexpr (CV::kPaged) {
+                                const uint32_t row = 16u * kk, in_box = row & (box_rows - 1);
+                                voff = (row - in_box) * 256u + in_box * 128u;
+                            }
+                            ptx::mma_bf16_ss_pair(tmem_base + 128 * i, da, db + (voff >> 4), C::kIdescPV,
                                                   (first && kk == 0) ? 0u : 1u);
                         }
                         ptx::mma_commit_pair_mc(v_empty + vs, kBoth);
@@ -472,7 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         const int r = L_id & 63;            // query row within this CTA's 64
         const int h = L_id >> 6;            // which 64 keys of the tile (S), which 128 dv of each N=256 (O)
         const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
-        uint32_t tile_cnt = 0, sync_cnt = 0;
+        uint32_t tile_cnt = 0, sync_cnt = 0, here_cnt = 0;
         bool ok = true;
         // scores are scaled by cs before exp2; a non-positive scale is applied to
         // the raw scores up front (cs = 1 after that), so that the row max of the
@@ -488,10 +629,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         while (ok && walker.next(pc)) {
             float m_ref = -INFINITY;  // reference max (base 2) of the row, the same in both of its threads
             float l_part = 0.f;       // this thread's share of the row sum, relative to m_ref
+            SeqView view{};
+            RowRange seen{};          // paged: the rows this thread's query row sees
+            if constexpr (CV::kPaged) {
+                view = view_of(pa, paged_len(pa, pc.b));
+                seen = token_rows(pa, view, (g * 128 + static_cast<int>(rank) * 64 + r) / pa.mask_rows);
+            }
             for (int t = pc.tile_lo; t < pc.tile_hi; ++t) {
                 const bool first = (t == pc.tile_lo);
                 int row0 = t * kTileKV;
-                if (row0 + kTileKV > pc.L) row0 = pc.L - kTileKV;
+                if (!CV::kPaged && row0 + kTileKV > pc.L) row0 = pc.L - kTileKV;
                 const int kv0 = row0 + 64 * h;       // key of column j is kv0 + j
                 const int lo = t * kTileKV;          // keys below lo belong to the previous tile
                 const uint32_t buf = tile_cnt % NS;
@@ -518,7 +665,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 }
                 // only the end-aligned last tile of a sequence holds keys of the
                 // previous tile (below lo); every key of a tile is below L
-                if (row0 < lo) {
+                if constexpr (CV::kPaged) {
+                    if (!seen.all(kv0, 64)) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (!seen.sees(kv0 + j)) x[j] = -INFINITY;
+                    }
+                } else if (row0 < lo) {
 #pragma unroll
                     for (int j = 0; j < 64; ++j)
                         if (kv0 + j < lo) x[j] = -INFINITY;
@@ -536,7 +689,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 // the row max outgrew the reference by more than 8 (p <= 2^8).
                 uint32_t packed[32];
                 float lsum = 0.f;
-                auto exps = [&](float m) {
+                auto exps = [&](float m_at) {
+                    // paged: a row that has seen no key yet (its scores all -inf)
+                    const float m = (CV::kPaged && m_at == -INFINITY) ? 0.f : m_at;
                     // the exponents and the row sum two lanes at a time (packed fp32)
                     float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
@@ -600,6 +755,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                     }
                     ptx::tmem_wait_st();
                 }
+                if constexpr (CV::kPaged) {
+                    // values of rows that no token sees: P is 0 there, and 0 times
+                    // whatever the page holds must be 0
+                    if (tile_unseen(pa, view, t)) {
+                        if (!leader && L_id == 0) ptx::mbar_arrive_expect_tx(v_here, 4);
+                        ok = ptx::mbar_wait_bounded_cluster(v_here, here_cnt & 1, tmo);
+                        if (!ok) break;
+                        ++here_cnt;
+                        if (unseen(pa, view, row0 + L_id)) {
+                            const uint32_t in_box = static_cast<uint32_t>(L_id) & (box_rows - 1);
+                            uint8_t* vrow = v_smem + (L_id - in_box) * 256u + in_box * 128u;
+#pragma unroll 1
+                            for (int i = 0; i < 2; ++i) {
+                                clear_row<128>(vrow + i * C::kVSlot, lane);
+                                clear_row<128>(vrow + i * C::kVSlot + box_rows * 128u, lane);
+                            }
+                        }
+                    }
+                }
                 uint8_t* prow = p_smem + pb * C::kPBuf + h * C::kPChunk + r * 128;
 #pragma unroll
                 for (int uu = 0; uu < 8; ++uu)
@@ -628,17 +802,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             if (!ok) break;
             const int qrow = g * 128 + static_cast<int>(rank) * 64 + r;  // row within the sequence
             float l_row = l_part + redsum[L_id ^ 64];
+            int slot = pc.slot;
+            if constexpr (CV::kPaged)
+                if (slot < 0 && pa.whole_slot >= 0) slot = pa.whole_slot + pc.b;
             // a sink applies once per row: to whole sequences here, to cut ones in the combine
             float o_fac = 1.f;
-            if (args.sinks != nullptr && pc.slot < 0)
-                o_fac = fold_sink(m_ref, l_row, args.sinks[qrow % args.H] * kLog2e);
-            const float inv_l = o_fac / l_row;
+            if (args.sinks != nullptr && slot < 0) {
+                const float s2 = args.sinks[qrow % args.H] * kLog2e;
+                o_fac = CV::kPaged ? fold_sink_any(m_ref, l_row, s2) : fold_sink(m_ref, l_row, s2);
+            }
+            const float inv_l = (CV::kPaged && l_row == 0.f) ? 0.f : o_fac / l_row;
             if (h == 0) {
                 const float lse_nat = (m_ref + log2f(l_row)) * 0.69314718055994530942f;
-                if (pc.slot < 0)
+                if (slot < 0)
                     args.lse[static_cast<size_t>(pc.b) * args.R + qrow] = lse_nat;
                 else
-                    args.part_lse[static_cast<size_t>(pc.slot) * args.R + qrow] = lse_nat;
+                    args.part_lse[static_cast<size_t>(slot) * args.R + qrow] = lse_nat;
             }
             // O / l leaves TMEM one 128-byte column block at a time: this warp's
             // 32 rows x 128 bytes are written into a 4 KB stage in the 128-byte
@@ -650,8 +829,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             {
                 constexpr int NST = C::kStagesPerWarp;
                 uint8_t* stage = p_smem + warp * (NST * 4096);
-                const bool partial = (pc.slot >= 0);
-                const int y0 = (partial ? pc.slot : pc.b) * args.R + g * 128 + static_cast<int>(rank) * 64 +
+                const bool partial = (slot >= 0);
+                const int y0 = (partial ? slot : pc.b) * args.R + g * 128 + static_cast<int>(rank) * 64 +
                                32 * (warp & 1);  // first of this warp's 32 rows
                 const int nblk = partial ? 8 : 4;  // fp32: 32 columns per box; bf16: 64
 #pragma unroll 1

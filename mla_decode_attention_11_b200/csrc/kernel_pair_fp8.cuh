@@ -185,13 +185,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         ptx::tmem_relinquish_pair();
     }
     if (warp == 0) {
-        const ScheduleScan sc = schedule_scan_warp(args.seqlens, args.B, args.L_max, args.P, args.split_tiles);
+        const ScheduleScan sc = schedule_scan_warp(SeqLens{args.seqlens, args.L_max}, args.B, args.P, args.split_tiles);
         const int S_eff = sc.S;
         const long long total = sc.units;
         const long long T = (total + args.P - 1) / args.P;
         int bf;
         long long af;
-        locate_warp(args.seqlens, args.B, args.L_max, S_eff, static_cast<long long>(p) * T, &bf, &af);
+        locate_warp(SeqLens{args.seqlens, args.L_max}, args.B, S_eff, static_cast<long long>(p) * T, &bf, &af);
         if (lane == 0) {
             *b_first_slot = bf;
             *acc_first_slot = af;
@@ -221,9 +221,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     {
         const long long total = *total_slot;
         const long long T = (total + args.P - 1) / args.P;
-        walker.seqlens = args.seqlens;
+        walker.lens = SeqLens{args.seqlens, args.L_max};
         walker.B = args.B;
-        walker.L_max = args.L_max;
         walker.p = p;
         walker.S = *split_slot;
         walker.k = 0;

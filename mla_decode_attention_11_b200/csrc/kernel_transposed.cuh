@@ -42,6 +42,7 @@
 #include <cuda_fp8.h>
 #include <cstdint>
 
+#include "paged.cuh"
 #include "ptx.cuh"
 #include "schedule.cuh"
 
@@ -113,6 +114,12 @@ __device__ __forceinline__ float fold_sink(float& m, float& l, float s2) {
     l = l * c + exp2f(s2 - mn);
     m = mn;
     return c;
+}
+
+// fold_sink for rows that may have no keys at all (m = -inf, l = 0): those keep
+// l = 0 when there is no sink either.
+__device__ __forceinline__ float fold_sink_any(float& m, float& l, float s2) {
+    return fmaxf(m, s2) == -INFINITY ? 1.f : fold_sink(m, l, s2);
 }
 
 constexpr float kLog2e = 1.4426950408889634074f;
@@ -298,11 +305,19 @@ __device__ __forceinline__ int group_row(const MainArgs& a, int G, int g, int j)
     return (j / gq) * a.H + g * gq + (j % gq);
 }
 
-template <int G, class SH = MlaShape>
+//
+// CV: where the kv rows are (paged.cuh).  In pages, the maps' outer dimensions
+// are (row of a page, page), a tile is 128 / box boxes stacked in the same
+// layout, each issued by its own lane of the producer warp, and the rows a
+// query row sees depend on its token.
+template <int G, class SH = MlaShape, class CV = ContigKv>
 __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
     mla_decode_transposed_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
-                                 const __grid_constant__ CUtensorMap tm_v, const MainArgs args) {
+                                 const __grid_constant__ CUtensorMap tm_v, const MainArgs args,
+                                 const __grid_constant__ typename CV::Args pa) {
     using C = TransposedCfg<G, SH>;
+    using Walker = PieceWalkerOf<typename CV::Lens>;
+    static_assert(!(SH::kFp8 && CV::kPaged), "the paged cache holds bf16 rows");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 
@@ -372,7 +387,7 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
         ptx::tmem_relinquish();
     }
     if (warp == 0) {
-        const ScheduleScan sc = schedule_scan_warp(args.seqlens, args.B, args.L_max, args.P, args.split_tiles);
+        const ScheduleScan sc = schedule_scan_warp(make_lens(args, pa), args.B, args.P, args.split_tiles);
         const int S_eff = sc.S;
         // partition bounds in the flat tile space, and the first sequence
         const long long total = sc.units;
@@ -380,7 +395,7 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
         const long long start = static_cast<long long>(p) * T;
         int bf;
         long long af;
-        locate_warp(args.seqlens, args.B, args.L_max, S_eff, start, &bf, &af);
+        locate_warp(make_lens(args, pa), args.B, S_eff, start, &bf, &af);
         if (lane == 0) {
             *b_first_slot = bf;
             *acc_first_slot = af;
@@ -410,13 +425,12 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
     // dependent) may start scheduling its CTAs; it waits for this grid's results
     ptx::launch_dependents();
 
-    PieceWalker walker;
+    Walker walker;
     {
         const long long total = *total_slot;
         const long long T = (total + args.P - 1) / args.P;
-        walker.seqlens = args.seqlens;
+        walker.lens = make_lens(args, pa);
         walker.B = args.B;
-        walker.L_max = args.L_max;
         walker.p = p;
         walker.S = *split_slot;
         walker.k = 0;
@@ -429,14 +443,106 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
 
     if (warp == 4) {
         // ============================================================ TMA producer
-        if (ptx::elect_one()) {
+        if constexpr (CV::kPaged) {
+            // the whole warp walks; lane l issues box l of each tile, lane 0 Q
+            uint32_t pair_cnt = 0, rope_cnt = 0, piece_cnt = 0;
+            int unit = 0;
+            bool ok = true;
+            const bool issues = lane < (kTileKV >> pa.box_log2);
+            const uint32_t dst_off = static_cast<uint32_t>(lane << pa.box_log2) * 128;  // a box row is 128 bytes
+            BoxStream<Walker> boxes(pa, walker, issues ? lane << pa.box_log2 : kTileKV);
+            Box ahead = boxes.next();  // the table entry of the next tile is on its way while a tile is issued
+            Piece pc;
+            while (ok && walker.next(pc)) {
+                if (piece_cnt > 0) ok = ptx::mbar_wait_bounded(q_empty, (piece_cnt - 1) & 1, tmo);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    const bool skip = blockIdx.x == 0 && unit == args.stall_unit;
+                    if constexpr (SH::kMha) {
+                        const int gq = args.H / args.Hkv;
+                        ptx::mbar_arrive_expect_tx(q_full, SH::kQKChunks * args.Sq * gq * 128);
+                        if (!skip)
+                            for (int c = 0; c < SH::kQKChunks; ++c)
+                                ptx::tma_load_4d(q_smem + c * C::kQChunkBytes, &tm_q, q_full, c * kChunk, g * gq, 0,
+                                                 pc.b);
+                    } else {
+                        ptx::mbar_arrive_expect_tx(q_full, kNumChunks * C::kQChunkBytes);
+                        if (!skip)
+                            for (int c = 0; c < kNumChunks; ++c)
+                                ptx::tma_load_2d(q_smem + c * C::kQChunkBytes, &tm_q, q_full, c * kChunk,
+                                                 pc.b * args.R + g * G);
+                    }
+                }
+                ++unit;
+                for (int t = pc.tile_lo; t < pc.tile_hi && ok; ++t) {
+                    const Box box = ahead;
+                    ahead = boxes.next();
+                    const int page = issues ? usable(pa, box, args.status) : 0;
+                    auto arm = [&](uint64_t* full, uint64_t* empty, uint32_t cnt, uint32_t slots, uint32_t bytes) {
+                        ok = ptx::mbar_wait_bounded(empty, ((cnt / slots) & 1) ^ 1, tmo);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) return false;
+                        if (lane == 0) ptx::mbar_arrive_expect_tx(full, bytes);
+                        __syncwarp();
+                        return issues && !(blockIdx.x == 0 && unit == args.stall_unit);
+                    };
+                    if constexpr (!SH::kMha) {
+                        const uint32_t s = rope_cnt % C::NR;
+                        if (arm(rope_full + s, rope_empty + s, rope_cnt, C::NR, C::kChunkBytes))
+                            ptx::tma_load_3d(rope_smem + s * C::kChunkBytes + dst_off, &tm_kv, rope_full + s,
+                                             8 * kChunk, box.row, page);
+                        if (!ok) break;
+                        ++unit;
+                        ++rope_cnt;
+                    }
+                    for (int pp = 0; pp < (SH::kMha ? 2 : 4); ++pp) {
+                        const uint32_t s = pair_cnt % C::NP;
+                        if (arm(pair_full + s, pair_empty + s, pair_cnt, C::NP, C::kPairBytes)) {
+                            uint8_t* dst = pair_smem + s * C::kPairBytes + dst_off;
+                            if constexpr (SH::kMha) {  // the tile's K rows, then its V rows (kv head g)
+                                const CUtensorMap* tm = (pp == 0) ? &tm_kv : &tm_v;
+                                ptx::tma_load_4d(dst, tm, pair_full + s, 0, g, box.row, page);
+                                ptx::tma_load_4d(dst + C::kChunkBytes, tm, pair_full + s, kChunk, g, box.row, page);
+                            } else {
+                                ptx::tma_load_3d(dst, &tm_kv, pair_full + s, (2 * pp) * kChunk, box.row, page);
+                                ptx::tma_load_3d(dst + C::kChunkBytes, &tm_kv, pair_full + s, (2 * pp + 1) * kChunk,
+                                                 box.row, page);
+                            }
+                        }
+                        if (!ok) break;
+                        ++unit;
+                        ++pair_cnt;
+                    }
+                }
+                ++piece_cnt;
+            }
+            if (!ok && lane == 0) {
+                atomicOr(args.status, kStatusTimeout);
+                *abort_flag = 1;
+            }
+            // drain: every armed load must have landed before the CTA can exit (bounded)
+            if (lane == 0) {
+                if (piece_cnt > 0) ptx::mbar_wait_bounded(q_full, (piece_cnt - 1) & 1, tmo);
+                for (uint32_t i = 0; i < C::NP && i < pair_cnt; ++i) {
+                    const uint32_t use = pair_cnt - 1 - i;
+                    ptx::mbar_wait_bounded(pair_full + (use % C::NP), (use / C::NP) & 1, tmo);
+                }
+                for (uint32_t i = 0; i < C::NR && i < rope_cnt; ++i) {
+                    const uint32_t use = rope_cnt - 1 - i;
+                    ptx::mbar_wait_bounded(rope_full + (use % C::NR), (use / C::NR) & 1, tmo);
+                }
+            }
+        } else if (ptx::elect_one()) {
             uint32_t pair_cnt = 0, rope_cnt = 0, piece_cnt = 0, f8_cnt = 0;
             int unit = 0;
             // FP8 cache: L2 prefetch cursor `prefetch_tiles` tiles ahead of the
             // staging loads, across piece boundaries (a tile's 9 chunk boxes,
             // and the next piece's Q rows on entering it).  The staging ring
             // holds few bytes, so without it the loads see HBM latency.
-            PieceWalker pf_walker = walker;
+            Walker pf_walker = walker;
             Piece pf_pc{};
             bool pf_live = false, pf_started = false;
             int pf_t = 0;
@@ -730,6 +836,8 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
         };
         Piece pc;
         while (ok && walker.next(pc)) {
+            SeqView view{};
+            if constexpr (CV::kPaged) view = view_of(pa, paged_len(pa, pc.b));
             float m_ref[G];
             float l_part[G];
 #pragma unroll
@@ -740,9 +848,9 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
             for (int t = pc.tile_lo; t < pc.tile_hi; ++t) {
                 const bool first = (t == pc.tile_lo);
                 int row0 = t * kTileKV;
-                if (row0 + kTileKV > pc.L) row0 = pc.L - kTileKV;
+                if (!CV::kPaged && row0 + kTileKV > pc.L) row0 = pc.L - kTileKV;
                 const int kv_row = row0 + row_in_tile;
-                const bool valid = (kv_row >= t * kTileKV) && (kv_row < pc.L);
+                const bool valid = CV::kPaged || ((kv_row >= t * kTileKV) && (kv_row < pc.L));
 
                 ok = ptx::mbar_wait_bounded(s_full, tile_cnt & 1, tmo);
                 if (!ok) break;
@@ -759,6 +867,9 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                             x[c0 + j] = valid ? __uint_as_float(r[j]) * args.scale_log2 : -INFINITY;
                     }
                 }
+                if constexpr (CV::kPaged)
+                    mask_columns<G>(pa, view, x, row0, kv_row, SH::kMha ? 0 : g * G,
+                                    SH::kMha ? args.H / args.Hkv : args.H, args.Sq - 1);
                 // column max over the tile's 128 kv rows
                 float* redmax = red + (tile_cnt & 1) * 4 * G;
                 const float wmax = warp_reduce_scatter<G, true>(x, lane);
@@ -791,7 +902,8 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < G; ++j) {
                         const float mn = fmaxf(m_ref[j], tmax[j]);
-                        alpha[j] = ex2_approx(m_ref[j] - mn);
+                        // paged: a column that has seen no key yet (both -inf) stays as it is
+                        alpha[j] = (CV::kPaged && m_ref[j] == mn) ? 1.f : ex2_approx(m_ref[j] - mn);
                         m_ref[j] = mn;
                         l_part[j] *= alpha[j];
                     }
@@ -815,8 +927,10 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                 uint32_t packed[G / 2];
 #pragma unroll
                 for (int j = 0; j < G; j += 2) {
-                    const float p0 = ex2_approx(x[j] - m_ref[j]);
-                    const float p1 = ex2_approx(x[j + 1] - m_ref[j + 1]);
+                    const float m0 = (CV::kPaged && m_ref[j] == -INFINITY) ? 0.f : m_ref[j];
+                    const float m1 = (CV::kPaged && m_ref[j + 1] == -INFINITY) ? 0.f : m_ref[j + 1];
+                    const float p0 = ex2_approx(x[j] - m0);
+                    const float p1 = ex2_approx(x[j + 1] - m1);
                     l_part[j] += p0;
                     l_part[j + 1] += p1;
                     if constexpr (SH::kFp8) {
@@ -832,6 +946,30 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                     const uint32_t off = swz_offset(row_in_tile, u, 2 * G);
                     *reinterpret_cast<uint4*>(pt_smem + off) =
                         make_uint4(packed[4 * u + 0], packed[4 * u + 1], packed[4 * u + 2], packed[4 * u + 3]);
+                }
+                if constexpr (CV::kPaged) {
+                    // values of rows that no token sees: P is 0 there, and 0 times
+                    // whatever the page holds must be 0
+                    if (tile_unseen(pa, view, t)) {
+                        if constexpr (SH::kMha) {  // V has its own slot (S^T waited for K only)
+                            const uint32_t use = 2 * tile_cnt + 1, vs = use % C::NP;
+                            ok = ptx::mbar_wait_bounded(pair_full + vs, (use / C::NP) & 1, tmo);
+                            if (!ok) break;
+                            if (unseen(pa, view, kv_row)) {
+                                uint8_t* vrow = pair_smem + vs * C::kPairBytes + row_in_tile * 128;
+                                clear_row<128>(vrow, lane);
+                                clear_row<128>(vrow + C::kChunkBytes, lane);
+                            }
+                        } else if (unseen(pa, view, kv_row)) {
+#pragma unroll 1
+                            for (uint32_t pp = 0; pp < 4; ++pp) {
+                                uint8_t* vrow =
+                                    pair_smem + ((4 * tile_cnt + pp) % C::NP) * C::kPairBytes + row_in_tile * 128;
+                                clear_row<128>(vrow, lane);
+                                clear_row<128>(vrow + C::kChunkBytes, lane);
+                            }
+                        }
+                    }
                 }
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_before();
@@ -852,8 +990,11 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
             if (!ok) break;
             // MHA: columns past Sq * gq are padding
             const int n_cols = SH::kMha ? args.Sq * (args.H / args.Hkv) : G;
+            int slot = pc.slot;
+            if constexpr (CV::kPaged)
+                if (slot < 0 && pa.whole_slot >= 0) slot = pa.whole_slot + pc.b;
             // a sink applies once per row: to whole sequences here, to cut ones in the combine
-            const bool sink_here = (args.sinks != nullptr) && (pc.slot < 0);
+            const bool sink_here = (args.sinks != nullptr) && (slot < 0);
             // thread j < G finishes query row j (sum, sink, lse) and leaves its
             // 1 / l in the max buffer the piece's last tile did not use
             float* fin = red + (tile_cnt & 1) * 4 * G;
@@ -866,13 +1007,16 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                     if (jj == j) mj = m_ref[jj];
                 float lj = redsum[0 * G + j] + redsum[1 * G + j] + redsum[2 * G + j] + redsum[3 * G + j];
                 float c = 1.f;
-                if (sink_here) c = fold_sink(mj, lj, args.sinks[qr % args.H] * kLog2e);
-                fin[j] = c / lj * args.o_scale;
+                if (sink_here) {
+                    const float s2 = args.sinks[qr % args.H] * kLog2e;
+                    c = CV::kPaged ? fold_sink_any(mj, lj, s2) : fold_sink(mj, lj, s2);
+                }
+                fin[j] = (CV::kPaged && lj == 0.f) ? 0.f : c / lj * args.o_scale;
                 const float lse_nat = (mj + log2f(lj)) * 0.69314718055994530942f;
-                if (pc.slot < 0)
+                if (slot < 0)
                     args.lse[static_cast<size_t>(pc.b) * args.R + qr] = lse_nat;
                 else
-                    args.part_lse[static_cast<size_t>(pc.slot) * args.R + qr] = lse_nat;
+                    args.part_lse[static_cast<size_t>(slot) * args.R + qr] = lse_nat;
             }
             ok = group_barrier();
             if (!ok) break;
@@ -884,7 +1028,7 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                     uint32_t r[16];
                     ptx::tmem_ld_16(lane_addr + blk * G + c0, r);
                     ptx::tmem_wait_ld();
-                    if (pc.slot < 0) {
+                    if (slot < 0) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             if (c0 + j >= n_cols) continue;
@@ -896,7 +1040,7 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                         for (int j = 0; j < 16; ++j) {
                             if (c0 + j >= n_cols) continue;
                             const size_t orow =
-                                static_cast<size_t>(pc.slot) * args.R + group_row<SH>(args, G, g, c0 + j);
+                                static_cast<size_t>(slot) * args.R + group_row<SH>(args, G, g, c0 + j);
                             args.part_o[orow * SH::kDv + dv] = __uint_as_float(r[j]) * fin[c0 + j];
                         }
                     }

@@ -74,27 +74,28 @@ Layout workspace_layout(long long slots, int R, int dv = mla::kDv) {
     return l;
 }
 
-template <int G, class SH = mla::MlaShape>
+template <int G, class SH = mla::MlaShape, class CV = mla::ContigKv>
 mla_status launch_transposed(const mla_plan& plan, const CUtensorMap& tm_q, const CUtensorMap& tm_kv,
-                             const CUtensorMap& tm_v, const mla::MainArgs& args, cudaStream_t stream) {
+                             const CUtensorMap& tm_v, const mla::MainArgs& args, const typename CV::Args& pa,
+                             cudaStream_t stream) {
     using C = mla::TransposedCfg<G, SH>;
-    auto kern = mla::mla_decode_transposed_kernel<G, SH>;
+    auto kern = mla::mla_decode_transposed_kernel<G, SH, CV>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
         return MLA_ERR_CUDA;
     const dim3 grid(static_cast<unsigned>(plan.num_partitions * plan.num_groups));
-    kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(tm_q, tm_kv, tm_v, args);
+    kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(tm_q, tm_kv, tm_v, args, pa);
     return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
-template <int G>
+template <int G, class CV = mla::ContigKv>
 mla_status launch_fp8mma(const mla_plan& plan, const CUtensorMap& tm_kv, const mla::MainArgs& args,
-                         cudaStream_t stream) {
+                         const typename CV::Args& pa, cudaStream_t stream) {
     using C = mla::Fp8MmaCfg<G>;
-    auto kern = mla::mla_decode_fp8mma_kernel<G>;
+    auto kern = mla::mla_decode_fp8mma_kernel<G, CV>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
         return MLA_ERR_CUDA;
     const dim3 grid(static_cast<unsigned>(plan.num_partitions * plan.num_groups));
-    kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(tm_kv, args);
+    kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(tm_kv, args, pa);
     return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
@@ -126,14 +127,16 @@ constexpr int kDefaultPrefetchTiles = 1;
 constexpr int kDefaultSplitTiles = 16;  // batch-invariant chunks: 16 tiles = 2048 keys
 using PairC = mla::PairCfg<kPairNK, kPairNV, kPairNS, kPairNP>;
 
+template <class CV = mla::ContigKv>
 mla_status launch_pair(const mla_plan& plan, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                        const CUtensorMap& tm_v, const CUtensorMap& tm_pf, const CUtensorMap& tm_out,
-                       const CUtensorMap& tm_part, const mla::MainArgs& args, cudaStream_t stream) {
-    auto kern = mla::mla_decode_pair_kernel<kPairNK, kPairNV, kPairNS, kPairNP>;
+                       const CUtensorMap& tm_part, const mla::MainArgs& args, const typename CV::Args& pa,
+                       cudaStream_t stream) {
+    auto kern = mla::mla_decode_pair_kernel<kPairNK, kPairNV, kPairNS, kPairNP, CV>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairC::kSmemBytes) != cudaSuccess)
         return MLA_ERR_CUDA;
     const dim3 grid(static_cast<unsigned>(2 * plan.num_partitions * plan.num_groups));
-    kern<<<grid, PairC::kThreads, PairC::kSmemBytes, stream>>>(tm_q, tm_k, tm_v, tm_pf, tm_out, tm_part, args);
+    kern<<<grid, PairC::kThreads, PairC::kSmemBytes, stream>>>(tm_q, tm_k, tm_v, tm_pf, tm_out, tm_part, args, pa);
     return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
@@ -164,14 +167,15 @@ bool encode_rows_store(EncodeTiledFn enc, CUtensorMap* m, const void* base, uint
                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The combine kernel is a programmatic dependent of the main kernel before it
-// on the stream: its CTAs may start (and scan the lengths) while the main
-// kernel finishes, and wait in the kernel for the main grid's results.
-template <int DV>
-mla_status launch_combine(dim3 grid, const mla::CombineArgs& c, cudaStream_t stream) {
+// A programmatic dependent of the kernel before it on the stream: its CTAs may
+// start (the combine scans the lengths) while that kernel finishes, and wait
+// in the kernel for that grid's results.
+template <class... Args, class... Given>
+mla_status launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t stream,
+                            const Given&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(mla::kCombineThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = 0;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -179,11 +183,17 @@ mla_status launch_combine(dim3 grid, const mla::CombineArgs& c, cudaStream_t str
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, mla::mla_decode_combine_kernel<DV>, c) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
         cudaGetLastError();
         return MLA_ERR_CUDA;
     }
     return MLA_OK;
+}
+
+template <int DV>
+mla_status launch_combine(dim3 grid, const mla::CombineArgs& c, cudaStream_t stream) {
+    return launch_dependent(mla::mla_decode_combine_kernel<DV>, grid, mla::kCombineThreads, stream, c,
+                            mla::ContigKv::Args{});
 }
 
 bool encode_2d_bf16(EncodeTiledFn enc, CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
@@ -287,6 +297,7 @@ const char* mla_status_string(mla_status s) {
         case MLA_ERR_CUDA: return "CUDA call failed";
         case MLA_ERR_TIMEOUT: return "device pipeline wait timed out; results invalid";
         case MLA_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
+        case MLA_ERR_PAGE: return "a block-table entry was outside the cache's pages";
         case MLA_ERR_SEQLEN: return "a sequence length was outside [0, L_max] (clamped)";
     }
     return "unknown status";
@@ -441,6 +452,7 @@ mla_status check_run_args(const mla_plan* plan, const void* q, const void* kv, c
     if (fp8 && !(std::isfinite(*kv_scale) && *kv_scale > 0.f)) return MLA_ERR_INVALID_ARG;
     const mla_plan& pl = *plan;
     const int R = pl.Sq * pl.H;
+    if (pl.page_size != 0) return MLA_ERR_INVALID_ARG;  // paged plans run through the paged entry points
     if (pl.B < 1 || pl.Sq < 1 || pl.H < 1 || pl.L_max < 1 || pl.num_partitions < 1 || pl.num_groups < 1 ||
         pl.group_rows * pl.num_groups != R)
         return MLA_ERR_INVALID_ARG;
@@ -559,17 +571,17 @@ mla_status launch_phases(const mla_plan& pl, const void* q, const void* kv, cons
     if (phases & 1) {
         mla_status st;
         if (pl.kernel == MLA_KERNEL_PAIR)
-            st = launch_pair(pl, tm_q, tm_k, tm_kv, tm_pf, tm_out, tm_part, a, stream);
+            st = launch_pair(pl, tm_q, tm_k, tm_kv, tm_pf, tm_out, tm_part, a, {}, stream);
         else if (pl.kernel == MLA_KERNEL_FP8_PAIR)
             st = launch_pair_fp8(pl, tm_k, tm_kv, tm_pf, tm_out, tm_part, a, stream);
         else if (pl.kernel == MLA_KERNEL_FP8_MMA)
-            st = (G == 16) ? launch_fp8mma<16>(pl, tm_kv, a, stream) : launch_fp8mma<32>(pl, tm_kv, a, stream);
+            st = (G == 16) ? launch_fp8mma<16>(pl, tm_kv, a, {}, stream) : launch_fp8mma<32>(pl, tm_kv, a, {}, stream);
         else if (fp8)
-            st = (G == 16) ? launch_transposed<16, mla::MlaFp8Shape>(pl, tm_q, tm_kv, tm_kv, a, stream)
-                           : launch_transposed<32, mla::MlaFp8Shape>(pl, tm_q, tm_kv, tm_kv, a, stream);
+            st = (G == 16) ? launch_transposed<16, mla::MlaFp8Shape>(pl, tm_q, tm_kv, tm_kv, a, {}, stream)
+                           : launch_transposed<32, mla::MlaFp8Shape>(pl, tm_q, tm_kv, tm_kv, a, {}, stream);
         else
-            st = (G == 16) ? launch_transposed<16>(pl, tm_q, tm_kv, tm_kv, a, stream)
-                           : launch_transposed<32>(pl, tm_q, tm_kv, tm_kv, a, stream);
+            st = (G == 16) ? launch_transposed<16>(pl, tm_q, tm_kv, tm_kv, a, {}, stream)
+                           : launch_transposed<32>(pl, tm_q, tm_kv, tm_kv, a, {}, stream);
         if (st != MLA_OK) {
             cudaGetLastError();
             return st;
@@ -658,6 +670,7 @@ mla_status mla_decode_check(const mla_plan* plan, void* workspace, void* stream)
     }
     if (st & mla::kStatusTimeout) return MLA_ERR_TIMEOUT;
     if (st & mla::kStatusSeqlen) return MLA_ERR_SEQLEN;
+    if (st & mla::kStatusPage) return MLA_ERR_PAGE;
     return MLA_OK;
 }
 
@@ -838,6 +851,7 @@ mla_status mha_run_phases(const mla_plan* plan, const void* q, const void* k, co
     if (!plan || !q || !k || !v || !seqlens || !out || !lse) return MLA_ERR_INVALID_ARG;
     if (!std::isfinite(softmax_scale)) return MLA_ERR_INVALID_ARG;
     const mla_plan& pl = *plan;
+    if (pl.page_size != 0) return MLA_ERR_INVALID_ARG;  // paged plans run through the paged entry points
     if (pl.kernel != MLA_KERNEL_MHA || pl.Hkv < 1 || pl.H < 1 || pl.H % pl.Hkv != 0 || pl.B < 1 || pl.Sq < 1 ||
         pl.L_max < 1 || pl.num_partitions < 1 || pl.num_groups != pl.Hkv || pl.head_dim != kMhaD ||
         pl.split_tiles < 0 || pl.split_tiles > (1 << 17))
@@ -908,8 +922,8 @@ mla_status mha_run_phases(const mla_plan* plan, const void* q, const void* k, co
     a.o_scale = 1.f;
     a.q = static_cast<const __nv_bfloat16*>(q);
     if (phases & 1) {
-        const mla_status st = (G == 16) ? launch_transposed<16, mla::MhaShape>(pl, tm_q, tm_k, tm_v, a, stream)
-                                        : launch_transposed<32, mla::MhaShape>(pl, tm_q, tm_k, tm_v, a, stream);
+        const mla_status st = (G == 16) ? launch_transposed<16, mla::MhaShape>(pl, tm_q, tm_k, tm_v, a, {}, stream)
+                                        : launch_transposed<32, mla::MhaShape>(pl, tm_q, tm_k, tm_v, a, {}, stream);
         if (st != MLA_OK) {
             cudaGetLastError();
             return st;
@@ -954,3 +968,5 @@ mla_status mha_decode_run_phase(const mla_plan* plan, const void* q, const void*
 }
 
 }  // extern "C"
+
+#include "paged_api.cuh"

@@ -1,0 +1,542 @@
+// paged_api.cuh -- host side of the paged-cache entry points (plans, argument
+// checks, tensor maps, launches).  Part of mla_decode.cu, which includes it
+// after its own helpers.
+#pragma once
+
+#include "kernel_append.cuh"
+#include "paged.cuh"
+
+namespace {
+
+constexpr int kMaxPageSize = 1 << 24;
+
+// The largest box (rows of one TMA load) that divides the page size, at most
+// `most`: 128 in the transposed kernel (a tile), 64 in the pair kernel (a CTA's
+// keys of a tile).  Fewer, larger loads: one costs its issuing thread a few
+// hundred cycles whatever it moves.
+int page_box(int page_size, int most) {
+    int box = most;
+    while (page_size % box != 0) box /= 2;
+    return box;
+}
+
+int box_log2(int box) { return box == 128 ? 7 : box == 64 ? 6 : box == 32 ? 5 : 4; }
+
+mla_status check_page_args(int32_t page_size, int32_t window, int32_t first_tokens) {
+    if (page_size < 1 || page_size > kMaxPageSize || window < 0 || first_tokens < 0 || first_tokens > (1 << 24))
+        return MLA_ERR_INVALID_ARG;
+    return page_size % 16 == 0 ? MLA_OK : MLA_ERR_UNSUPPORTED;
+}
+
+struct PrefixLayout {
+    size_t pre_lse, pre_o, own_lse, own_o, total;
+};
+
+// shared prefix: slots of the prefix's pieces (two per partition, one per
+// 128-row group) and of the sequences' own (two per partition, one per sequence)
+PrefixLayout prefix_layout(const mla_plan& pl) {
+    const size_t R = static_cast<size_t>(pl.Sq) * pl.H;
+    const size_t pre = 128 * (2 * static_cast<size_t>(pl.prefix_partitions) + pl.prefix_groups);
+    const size_t own = R * (2 * static_cast<size_t>(pl.num_partitions) + pl.B);
+    PrefixLayout l;
+    l.pre_lse = kHeaderBytes;
+    l.own_lse = align_up(l.pre_lse + pre * sizeof(float), 256);
+    l.pre_o = align_up(l.own_lse + own * sizeof(float), 256);
+    l.own_o = align_up(l.pre_o + pre * mla::kDv * sizeof(float), 256);
+    l.total = l.own_o + own * mla::kDv * sizeof(float);
+    return l;
+}
+
+// Latent pages [num_pages, page_size, 576]: boxes of `rows` rows x 64 columns x
+// `chunks` adjacent 64-column chunks, chunk after chunk in shared memory
+// (chunks = 1: a 3-D map {576, page_size, num_pages}).
+bool encode_pages(EncodeTiledFn enc, CUtensorMap* m, const void* kv, int page_size, int num_pages, int rows,
+                  int chunks) {
+    return chunks == 1 ? encode_kv(enc, m, kv, page_size, num_pages, rows)
+                       : encode_kv_chunks(enc, m, kv, page_size, num_pages, rows, chunks);
+}
+
+mla::PagedArgs paged_args(const mla_plan& pl, const int32_t* seqlens, const int32_t* table, int64_t table_stride,
+                          int32_t num_pages, bool pair) {
+    mla::PagedArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.seqlens = seqlens;
+    a.len_stride = 1;
+    a.table = table;
+    a.table_stride = table_stride;
+    a.L_max = pl.L_max;
+    a.num_pages = num_pages;
+    a.page_size = pl.page_size;
+    a.box = page_box(pl.page_size, pair ? 64 : 128);
+    a.box_log2 = box_log2(a.box);
+    a.Sq = pl.Sq;
+    // a window that no sequence can fill leaves nothing out
+    a.window = pl.window >= pl.L_max ? 0 : pl.window;
+    a.first = pl.first_tokens < pl.L_max ? pl.first_tokens : pl.L_max;
+    a.mask_rows = pl.H / pl.Hkv;
+    a.whole_slot = -1;
+    return a;
+}
+
+void main_args(mla::MainArgs& a, const mla_plan& pl, const int32_t* seqlens, float softmax_scale, const float* sinks,
+               void* out, float* lse, void* workspace, size_t lse_off, size_t o_off) {
+    std::memset(&a, 0, sizeof a);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.seqlens = seqlens;
+    a.B = pl.B;
+    a.R = pl.Sq * pl.H;
+    a.L_max = pl.L_max;
+    a.P = pl.num_partitions;
+    a.NG = pl.num_groups;
+    a.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634074);
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.lse = lse;
+    a.part_o = reinterpret_cast<float*>(ws + o_off);
+    a.part_lse = reinterpret_cast<float*>(ws + lse_off);
+    a.status = reinterpret_cast<uint32_t*>(ws);
+    const unsigned long long tmo = g_timeout_ns.load();
+    a.timeout_ns = tmo ? tmo : kDefaultTimeoutNs;
+    a.stall_unit = g_stall_unit.load();
+    a.prefetch_tiles = pl.l2_prefetch_tiles;
+    a.sinks = sinks;
+    a.H = pl.H;
+    a.Sq = pl.Sq;
+    a.Hkv = pl.Hkv;
+    a.o_scale = 1.f;
+}
+
+// What every paged decode checks of its plan (but the plan's kind) and pointers.
+mla_status check_paged(const mla_plan* plan, const void* q, const void* k, const void* v, int32_t num_pages,
+                       const int32_t* table, int64_t table_stride, int32_t table_width, const int32_t* seqlens,
+                       float softmax_scale, const float* sinks, const void* out, const float* lse) {
+    if (!plan || !q || !k || !v || !table || !seqlens || !out || !lse) return MLA_ERR_INVALID_ARG;
+    if (!std::isfinite(softmax_scale)) return MLA_ERR_INVALID_ARG;
+    const mla_plan& pl = *plan;
+    if (pl.B < 1 || pl.Sq < 1 || pl.H < 1 || pl.Hkv < 1 || pl.L_max < 1 || pl.num_partitions < 1 ||
+        pl.num_partitions > 4096 || pl.num_groups < 1 || pl.split_tiles != 0 || pl.l2_prefetch_tiles < 0 ||
+        pl.l2_prefetch_tiles > 16 || pl.page_size < 1 || check_page_args(pl.page_size, pl.window, pl.first_tokens) != MLA_OK)
+        return MLA_ERR_INVALID_ARG;
+    if (num_pages < 1 || table_stride < 0 || table_width < 1 ||
+        static_cast<int64_t>(table_width) * pl.page_size < pl.L_max)
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+        !aligned(seqlens, 4) || !aligned(table, 4) || !aligned(sinks, 4))
+        return MLA_ERR_ALIGNMENT;
+    return MLA_OK;
+}
+
+bool mla_groups_ok(const mla_plan& pl) {
+    const int R = pl.Sq * pl.H;
+    if (pl.Hkv != 1 || pl.head_dim != mla::kDqk || pl.group_rows * pl.num_groups != R) return false;
+    if (pl.kernel == MLA_KERNEL_PAIR) return pl.group_rows == 128;
+    return pl.kernel == MLA_KERNEL_TRANSPOSED && (pl.group_rows == 16 || pl.group_rows == 32);
+}
+
+// The main kernel of an MLA plan over pages.
+mla_status launch_mla_paged(EncodeTiledFn enc, const mla_plan& pl, const void* q, uint64_t q_rows, const void* kv,
+                            const mla::MainArgs& a, const mla::PagedArgs& pa, uint64_t part_rows, cudaStream_t stream) {
+    CUtensorMap tm_q, tm_k, tm_v, tm_pf, tm_out, tm_part;
+    if (pl.kernel == MLA_KERNEL_PAIR) {
+        if (!encode_q_chunks(enc, &tm_q, q, q_rows) ||
+            !encode_pages(enc, &tm_k, kv, pa.page_size, pa.num_pages, pa.box, 1) ||
+            !encode_pages(enc, &tm_v, kv, pa.page_size, pa.num_pages, pa.box, 2) ||
+            !encode_pages(enc, &tm_pf, kv, pa.page_size, pa.num_pages, pa.box, mla::kNumChunks) ||
+            !encode_rows_store(enc, &tm_out, a.out, q_rows, false) ||
+            !encode_rows_store(enc, &tm_part, a.part_o, part_rows, true))
+            return MLA_ERR_CUDA;
+        return launch_pair<mla::PagedKv>(pl, tm_q, tm_k, tm_v, tm_pf, tm_out, tm_part, a, pa, stream);
+    }
+    if (!encode_2d_bf16(enc, &tm_q, q, mla::kDqk, q_rows, mla::kChunk, pl.group_rows) ||
+        !encode_pages(enc, &tm_k, kv, pa.page_size, pa.num_pages, pa.box, 1))
+        return MLA_ERR_CUDA;
+    return pl.group_rows == 16
+               ? launch_transposed<16, mla::MlaShape, mla::PagedKv>(pl, tm_q, tm_k, tm_k, a, pa, stream)
+               : launch_transposed<32, mla::MlaShape, mla::PagedKv>(pl, tm_q, tm_k, tm_k, a, pa, stream);
+}
+
+mla::CombineArgs combine_args(const mla::MainArgs& a) {
+    mla::CombineArgs c;
+    std::memset(&c, 0, sizeof c);
+    c.seqlens = a.seqlens;
+    c.B = a.B;
+    c.R = a.R;
+    c.L_max = a.L_max;
+    c.P = a.P;
+    c.out = a.out;
+    c.lse = a.lse;
+    c.part_o = a.part_o;
+    c.part_lse = a.part_lse;
+    c.sinks = a.sinks;
+    c.H = a.H;
+    return c;
+}
+
+dim3 combine_grid(const mla_plan& pl) {
+    return dim3(static_cast<unsigned>(pl.B),
+                static_cast<unsigned>(mla::combine_grid_y(pl.B, pl.Sq * pl.H, pl.num_sms)));
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status mla_decode_plan_paged(int32_t B, int32_t Sq, int32_t H, int32_t L_max, int32_t page_size, int32_t window,
+                                 int32_t first_tokens, int32_t device, int32_t num_partitions_override,
+                                 mla_plan* plan, size_t* workspace_bytes) {
+    if (!plan) return MLA_ERR_INVALID_ARG;
+    mla_plan p;
+    mla_status st = mla_decode_plan_kernel(B, Sq, H, L_max, device, num_partitions_override, 0, &p, nullptr);
+    if (st == MLA_OK) st = check_page_args(page_size, window, first_tokens);
+    if (st != MLA_OK) return st;
+    p.page_size = page_size;
+    p.window = window;
+    p.first_tokens = first_tokens;
+    *plan = p;
+    if (workspace_bytes) *workspace_bytes = p.workspace_bytes;
+    return MLA_OK;
+}
+
+mla_status mla_decode_run_paged(const mla_plan* plan, const void* q, const void* kv_pages, int32_t num_pages,
+                                const int32_t* block_table, int64_t table_stride, int32_t table_width,
+                                const int32_t* seqlens, float softmax_scale, const float* sinks, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream_) {
+    mla_status st = check_paged(plan, q, kv_pages, kv_pages, num_pages, block_table, table_stride, table_width, seqlens,
+                                softmax_scale, sinks, out, lse);
+    if (st != MLA_OK) return st;
+    const mla_plan& pl = *plan;
+    if (!mla_groups_ok(pl) || pl.prefix_max != 0) return MLA_ERR_INVALID_ARG;
+    const int R = pl.Sq * pl.H;
+    const Layout lay = workspace_layout(num_slots(pl), R);
+    if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
+    st = check_run_device(pl);
+    if (st != MLA_OK) return st;
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return MLA_ERR_CUDA;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    mla::MainArgs a;
+    main_args(a, pl, seqlens, softmax_scale, sinks, out, lse, workspace, lay.part_lse_off, lay.part_o_off);
+    const mla::PagedArgs pa =
+        paged_args(pl, seqlens, block_table, table_stride, num_pages, pl.kernel == MLA_KERNEL_PAIR);
+    st = launch_mla_paged(enc, pl, q, static_cast<uint64_t>(pl.B) * R, kv_pages, a, pa,
+                          static_cast<uint64_t>(num_slots(pl)) * R, stream);
+    if (st != MLA_OK) {
+        cudaGetLastError();
+        return st;
+    }
+    return launch_dependent(mla::mla_decode_combine_kernel<mla::kDv, mla::PagedKv>, combine_grid(pl),
+                            mla::kCombineThreads, stream, combine_args(a), pa);
+}
+
+mla_status mla_decode_plan_paged_fp8(int32_t B, int32_t Sq, int32_t H, int32_t L_max, int32_t page_size,
+                                     int32_t window, int32_t first_tokens, int32_t device,
+                                     int32_t num_partitions_override, mla_plan* plan, size_t* workspace_bytes) {
+    if (!plan) return MLA_ERR_INVALID_ARG;
+    mla_plan p;
+    mla_status st = mla_decode_plan_fp8_kernel(B, Sq, H, L_max, device, num_partitions_override, MLA_KERNEL_FP8_MMA, &p,
+                                               nullptr);
+    if (st == MLA_OK) st = check_page_args(page_size, window, first_tokens);
+    if (st != MLA_OK) return st;
+    p.page_size = page_size;
+    p.window = window;
+    p.first_tokens = first_tokens;
+    *plan = p;
+    if (workspace_bytes) *workspace_bytes = p.workspace_bytes;
+    return MLA_OK;
+}
+
+mla_status mla_decode_run_paged_fp8(const mla_plan* plan, const void* q, const void* kv_pages, int32_t num_pages,
+                                    float kv_scale, const int32_t* block_table, int64_t table_stride,
+                                    int32_t table_width, const int32_t* seqlens, float softmax_scale,
+                                    const float* sinks, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                    void* stream_) {
+    mla_status st = check_paged(plan, q, kv_pages, kv_pages, num_pages, block_table, table_stride, table_width, seqlens,
+                                softmax_scale, sinks, out, lse);
+    if (st != MLA_OK) return st;
+    const mla_plan& pl = *plan;
+    const int R = pl.Sq * pl.H, G = pl.group_rows;
+    if (pl.kernel != MLA_KERNEL_FP8_MMA || pl.Hkv != 1 || pl.head_dim != mla::kDqk || (G != 16 && G != 32) ||
+        G * pl.num_groups != R || pl.prefix_max != 0 || !(std::isfinite(kv_scale) && kv_scale > 0.f))
+        return MLA_ERR_INVALID_ARG;
+    const Layout lay = workspace_layout(num_slots(pl), R);
+    if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
+    st = check_run_device(pl);
+    if (st != MLA_OK) return st;
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return MLA_ERR_CUDA;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    mla::MainArgs a;
+    main_args(a, pl, seqlens, softmax_scale, sinks, out, lse, workspace, lay.part_lse_off, lay.part_o_off);
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * kv_scale * 1.4426950408889634074);
+    a.o_scale = kv_scale;
+    const mla::PagedArgs pa = paged_args(pl, seqlens, block_table, table_stride, num_pages, false);
+    CUtensorMap tm_kv;
+    if (!encode_kv_fp8(enc, &tm_kv, kv_pages, pl.page_size, num_pages, pa.box)) return MLA_ERR_CUDA;
+    st = (G == 16) ? launch_fp8mma<16, mla::PagedKv>(pl, tm_kv, a, pa, stream)
+                   : launch_fp8mma<32, mla::PagedKv>(pl, tm_kv, a, pa, stream);
+    if (st != MLA_OK) {
+        cudaGetLastError();
+        return st;
+    }
+    return launch_dependent(mla::mla_decode_combine_kernel<mla::kDv, mla::PagedKv>, combine_grid(pl),
+                            mla::kCombineThreads, stream, combine_args(a), pa);
+}
+
+mla_status mha_decode_plan_paged(int32_t B, int32_t Sq, int32_t H, int32_t Hkv, int32_t L_max, int32_t page_size,
+                                 int32_t window, int32_t first_tokens, int32_t device,
+                                 int32_t num_partitions_override, mla_plan* plan, size_t* workspace_bytes) {
+    if (!plan) return MLA_ERR_INVALID_ARG;
+    mla_plan p;
+    mla_status st = mha_decode_plan(B, Sq, H, Hkv, L_max, device, num_partitions_override, &p, nullptr);
+    if (st == MLA_OK) st = check_page_args(page_size, window, first_tokens);
+    if (st != MLA_OK) return st;
+    p.page_size = page_size;
+    p.window = window;
+    p.first_tokens = first_tokens;
+    *plan = p;
+    if (workspace_bytes) *workspace_bytes = p.workspace_bytes;
+    return MLA_OK;
+}
+
+mla_status mha_decode_run_paged(const mla_plan* plan, const void* q, const void* k_pages, const void* v_pages,
+                                int32_t num_pages, const int32_t* block_table, int64_t table_stride,
+                                int32_t table_width, const int32_t* seqlens, float softmax_scale, const float* sinks,
+                                void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream_) {
+    mla_status st = check_paged(plan, q, k_pages, v_pages, num_pages, block_table, table_stride, table_width, seqlens,
+                                softmax_scale, sinks, out, lse);
+    if (st != MLA_OK) return st;
+    const mla_plan& pl = *plan;
+    const int G = pl.group_rows;
+    if (pl.kernel != MLA_KERNEL_MHA || pl.H % pl.Hkv != 0 || pl.num_groups != pl.Hkv || pl.head_dim != kMhaD ||
+        (G != 16 && G != 32) || pl.Sq * (pl.H / pl.Hkv) > G || pl.prefix_max != 0)
+        return MLA_ERR_INVALID_ARG;
+    const int R = pl.Sq * pl.H, gq = pl.H / pl.Hkv;
+    const Layout lay = workspace_layout(num_slots(pl), R, kMhaD);
+    if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
+    st = check_run_device(pl);
+    if (st != MLA_OK) return st;
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return MLA_ERR_CUDA;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    mla::MainArgs a;
+    main_args(a, pl, seqlens, softmax_scale, sinks, out, lse, workspace, lay.part_lse_off, lay.part_o_off);
+    const mla::PagedArgs pa = paged_args(pl, seqlens, block_table, table_stride, num_pages, false);
+    CUtensorMap tm_q, tm_k, tm_v;
+    const uint64_t dq[4] = {static_cast<uint64_t>(kMhaD), static_cast<uint64_t>(pl.H), static_cast<uint64_t>(pl.Sq),
+                            static_cast<uint64_t>(pl.B)};
+    const uint32_t bq[4] = {static_cast<uint32_t>(mla::kChunk), static_cast<uint32_t>(gq),
+                            static_cast<uint32_t>(pl.Sq), 1u};
+    const uint64_t dk[4] = {static_cast<uint64_t>(kMhaD), static_cast<uint64_t>(pl.Hkv),
+                            static_cast<uint64_t>(pl.page_size), static_cast<uint64_t>(num_pages)};
+    const uint32_t bk[4] = {static_cast<uint32_t>(mla::kChunk), 1u, static_cast<uint32_t>(pa.box), 1u};
+    if (!encode_4d_bf16(enc, &tm_q, q, dq, bq) || !encode_4d_bf16(enc, &tm_k, k_pages, dk, bk) ||
+        !encode_4d_bf16(enc, &tm_v, v_pages, dk, bk))
+        return MLA_ERR_CUDA;
+    st = (G == 16) ? launch_transposed<16, mla::MhaShape, mla::PagedKv>(pl, tm_q, tm_k, tm_v, a, pa, stream)
+                   : launch_transposed<32, mla::MhaShape, mla::PagedKv>(pl, tm_q, tm_k, tm_v, a, pa, stream);
+    if (st != MLA_OK) {
+        cudaGetLastError();
+        return st;
+    }
+    return launch_dependent(mla::mla_decode_combine_kernel<kMhaD, mla::PagedKv>, combine_grid(pl),
+                            mla::kCombineThreads, stream, combine_args(a), pa);
+}
+
+mla_status mla_decode_plan_prefix(int32_t B, int32_t Sq, int32_t H, int32_t L_max, int32_t prefix_max,
+                                  int32_t page_size, int32_t device, int32_t num_partitions_override, mla_plan* plan,
+                                  size_t* workspace_bytes) {
+    if (!plan || prefix_max < 1 || prefix_max > (1 << 24)) return MLA_ERR_INVALID_ARG;
+    mla_plan p;
+    mla_status st = mla_decode_plan_kernel(B, Sq, H, L_max, device, num_partitions_override, 0, &p, nullptr);
+    if (st == MLA_OK) st = check_page_args(page_size, 0, 0);
+    if (st != MLA_OK) return st;
+    p.page_size = page_size;
+    p.prefix_max = prefix_max;
+    p.prefix_groups = static_cast<int32_t>((static_cast<int64_t>(B) * Sq * H + 127) / 128);
+    int P = num_partitions_override > 0 ? num_partitions_override : p.num_sms / 2;  // one CTA pair each
+    if (P < 1) P = 1;
+    p.prefix_partitions = P > 4096 ? 4096 : P;
+    p.workspace_bytes = prefix_layout(p).total;
+    *plan = p;
+    if (workspace_bytes) *workspace_bytes = p.workspace_bytes;
+    return MLA_OK;
+}
+
+mla_status mla_decode_run_prefix(const mla_plan* plan, const void* q, const void* kv_pages, int32_t num_pages,
+                                 const int32_t* prefix_table, int32_t prefix_width, const int32_t* prefix_len,
+                                 const int32_t* block_table, int64_t table_stride, int32_t table_width,
+                                 const int32_t* seqlens, float softmax_scale, const float* sinks, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream_) {
+    mla_status st = check_paged(plan, q, kv_pages, kv_pages, num_pages, block_table, table_stride, table_width, seqlens,
+                                softmax_scale, sinks, out, lse);
+    if (st != MLA_OK) return st;
+    const mla_plan& pl = *plan;
+    const int R = pl.Sq * pl.H;
+    if (!prefix_table || !prefix_len || !mla_groups_ok(pl) || pl.window != 0 || pl.prefix_max < 1 ||
+        pl.prefix_max > (1 << 24) || pl.prefix_partitions < 1 || pl.prefix_partitions > 4096 ||
+        pl.prefix_groups != (static_cast<int64_t>(pl.B) * R + 127) / 128 || prefix_width < 1 ||
+        static_cast<int64_t>(prefix_width) * pl.page_size < pl.prefix_max)
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned(prefix_table, 4) || !aligned(prefix_len, 4)) return MLA_ERR_ALIGNMENT;
+    const PrefixLayout lay = prefix_layout(pl);
+    if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
+    st = check_run_device(pl);
+    if (st != MLA_OK) return st;
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return MLA_ERR_CUDA;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    const uint64_t q_rows = static_cast<uint64_t>(pl.B) * R;
+
+    // the prefix: one "sequence" per 128 rows of the batch, all reading the same
+    // pages; every piece leaves a partial (a sink enters once, at the merge)
+    mla_plan pre = pl;
+    pre.kernel = MLA_KERNEL_PAIR;
+    pre.B = pl.prefix_groups;
+    pre.Sq = 1;
+    pre.H = 128;
+    pre.L_max = pl.prefix_max;
+    pre.group_rows = 128;
+    pre.num_groups = 1;
+    pre.num_partitions = pl.prefix_partitions;
+    mla::MainArgs ap;
+    main_args(ap, pre, prefix_len, softmax_scale, nullptr, out, lse, workspace, lay.pre_lse, lay.pre_o);
+    mla::PagedArgs pp = paged_args(pre, prefix_len, prefix_table, 0, num_pages, true);
+    pp.len_stride = 0;
+    pp.whole_slot = 2 * pl.prefix_partitions;
+    st = launch_mla_paged(enc, pre, q, q_rows, kv_pages, ap, pp,
+                          128ull * (2ull * pl.prefix_partitions + pl.prefix_groups), stream);
+    if (st != MLA_OK) {
+        cudaGetLastError();
+        return st;
+    }
+    // the sequences' own keys
+    mla::MainArgs ao;
+    main_args(ao, pl, seqlens, softmax_scale, nullptr, out, lse, workspace, lay.own_lse, lay.own_o);
+    mla::PagedArgs po = paged_args(pl, seqlens, block_table, table_stride, num_pages, pl.kernel == MLA_KERNEL_PAIR);
+    po.whole_slot = 2 * pl.num_partitions;
+    st = launch_mla_paged(enc, pl, q, q_rows, kv_pages, ao, po,
+                          static_cast<uint64_t>(R) * (2ull * pl.num_partitions + pl.B), stream);
+    if (st != MLA_OK) {
+        cudaGetLastError();
+        return st;
+    }
+    mla::PrefixCombineArgs c;
+    c.B = pl.B;
+    c.R = R;
+    c.H = pl.H;
+    c.P_own = pl.num_partitions;
+    c.P_pre = pl.prefix_partitions;
+    c.groups = pl.prefix_groups;
+    c.out = ao.out;
+    c.lse = lse;
+    c.own_o = ao.part_o;
+    c.own_lse = ao.part_lse;
+    c.pre_o = ap.part_o;
+    c.pre_lse = ap.part_lse;
+    c.sinks = sinks;
+    return launch_dependent(mla::mla_prefix_combine_kernel, combine_grid(pl), mla::kCombineThreads, stream, c, po, pp);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Appending to a paged cache.
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// Checks what both kinds of append share and fills the kernel's arguments.
+mla_status append_args(const mla_append* p, bool mha, mla::AppendArgs& a) {
+    if (!p || !p->seqlens || !p->block_table || !p->cos_sin || !p->k_pages) return MLA_ERR_INVALID_ARG;
+    if (p->T != 0 && (!p->k || !p->v || (p->H > 0 && (!p->q_in || !p->q_out)))) return MLA_ERR_INVALID_ARG;
+    if (mha && !p->v_pages) return MLA_ERR_INVALID_ARG;
+    if (p->B < 1 || p->T < 0 || p->page_size < 1 || p->num_pages < 1 || p->table_width < 1 || p->table_stride < 0 ||
+        p->num_positions < 1 || p->H < 0 || p->H > 65535 || (p->interleaved != 0 && p->interleaved != 1))
+        return MLA_ERR_INVALID_ARG;
+    if (mha ? (p->Hkv < 1 || p->Hkv > 65535 || p->rope_dim < 16 || p->rope_dim > 128 || p->rope_dim % 16 != 0)
+            : p->rope_dim != 64)
+        return MLA_ERR_INVALID_ARG;
+    if (!p->cu_tokens && p->T % p->B != 0) return MLA_ERR_INVALID_ARG;
+    if (mha ? p->kv_scale != 0.f : !(std::isfinite(p->kv_scale) && p->kv_scale >= 0.f)) return MLA_ERR_INVALID_ARG;
+    if (!aligned(p->k, 16) || !aligned(p->v, 16) || !aligned(p->k_pages, 16) || !aligned(p->v_pages, 16) ||
+        !aligned(p->q_in, 16) || !aligned(p->q_out, 16) || !aligned(p->cos_sin, 16) || !aligned(p->seqlens, 4) ||
+        !aligned(p->cu_tokens, 4) || !aligned(p->block_table, 4) || !aligned(p->status, 4))
+        return MLA_ERR_ALIGNMENT;
+    const int64_t strides[] = {p->k_token_stride, p->k_head_stride, p->v_token_stride, p->v_head_stride,
+                               p->q_in_token_stride, p->q_in_head_stride, p->q_out_token_stride, p->q_out_head_stride};
+    for (int64_t s : strides)
+        if (s % 8 != 0) return MLA_ERR_ALIGNMENT;
+    std::memset(&a, 0, sizeof a);
+    a.B = p->B;
+    a.T = p->T;
+    a.per_seq = p->T / p->B;
+    a.cu = p->cu_tokens;
+    a.seqlens = p->seqlens;
+    a.table = p->block_table;
+    a.table_stride = p->table_stride;
+    a.table_width = p->table_width;
+    a.num_pages = p->num_pages;
+    a.page_size = p->page_size;
+    a.cos_sin = p->cos_sin;
+    a.num_positions = p->num_positions;
+    a.rot = p->rope_dim;
+    a.status = p->status;
+    a.k = static_cast<const __nv_bfloat16*>(p->k);
+    a.k_token = p->k_token_stride;
+    a.k_head = p->k_head_stride;
+    a.v = static_cast<const __nv_bfloat16*>(p->v);
+    a.v_token = p->v_token_stride;
+    a.v_head = p->v_head_stride;
+    a.q_in = static_cast<const __nv_bfloat16*>(p->q_in);
+    a.qi_token = p->q_in_token_stride;
+    a.qi_head = p->q_in_head_stride;
+    a.q_out = static_cast<__nv_bfloat16*>(p->q_out);
+    a.qo_token = p->q_out_token_stride;
+    a.qo_head = p->q_out_head_stride;
+    a.H = p->H;
+    a.Hkv = p->Hkv;
+    a.k_pages = p->k_pages;
+    a.v_pages = static_cast<__nv_bfloat16*>(p->v_pages);
+    a.kv_scale = p->kv_scale;
+    return MLA_OK;
+}
+
+mla_status launch_append(void (*kernel)(const mla::AppendArgs, int), const mla::AppendArgs& a, int tasks,
+                         cudaStream_t stream) {
+    if (a.T == 0) return MLA_OK;
+    mla_plan any;
+    any.device = -1;
+    const mla_status st = check_run_device(any);
+    if (st != MLA_OK) return st;
+    const int64_t warps = static_cast<int64_t>(a.T) * tasks, per = mla::kAppendThreads / 32;
+    const int64_t blocks = (warps + per - 1) / per;
+    if (blocks > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+    kernel<<<static_cast<unsigned>(blocks), mla::kAppendThreads, 0, stream>>>(a, tasks);
+    return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status mla_cache_append(const mla_append* args, void* stream) {
+    mla::AppendArgs a;
+    const mla_status st = append_args(args, false, a);
+    if (st != MLA_OK) return st;
+    const int per = mla::HeadRows<64>::kHeads, tasks = 1 + (a.H + per - 1) / per;
+    const bool fp8 = a.kv_scale > 0.f, il = args->interleaved != 0;
+    return launch_append(fp8 ? (il ? mla::mla_cache_append_kernel<true, true> : mla::mla_cache_append_kernel<true, false>)
+                             : (il ? mla::mla_cache_append_kernel<false, true> : mla::mla_cache_append_kernel<false, false>),
+                         a, tasks, static_cast<cudaStream_t>(stream));
+}
+
+mla_status mha_cache_append(const mla_append* args, void* stream) {
+    mla::AppendArgs a;
+    const mla_status st = append_args(args, true, a);
+    if (st != MLA_OK) return st;
+    const int per = mla::HeadRows<128>::kHeads, tasks = 2 * ((a.Hkv + per - 1) / per) + (a.H + per - 1) / per;
+    return launch_append(args->interleaved ? mla::mha_cache_append_kernel<true> : mla::mha_cache_append_kernel<false>,
+                         a, tasks, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -58,13 +58,12 @@ __device__ __forceinline__ long long num_units(int L, int S) {
     return S > 0 ? (n + S - 1) / S : n;
 }
 
-// Warp-cooperative: total tiles over all sequences, and (for `start`) the
-// first sequence whose tiles reach past `start` with its flat offset.
-// Every lane returns the same values.
-struct ScanResult {
-    long long total;     // N_t
-    int b_first;         // first sequence with acc_b + n_b > start (or B)
-    long long acc_first; // acc of b_first
+// Where the schedule's functions take a sequence's number of keys from (a
+// callable b -> keys).  SeqLens: an array of lengths on the device.
+struct SeqLens {
+    const int32_t* seqlens;
+    int L_max;
+    __device__ __forceinline__ int operator()(int b) const { return clamp_len(__ldg(seqlens + b), L_max, nullptr); }
 };
 
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
@@ -92,18 +91,25 @@ struct ScheduleScan {
     long long acc_at;  // units of the sequences before sequence `b_at` (0 when b_at < 0)
 };
 
+// The chunk size of a run whose plan leaves the choice (0: balanced).
+__device__ __forceinline__ int pick_schedule(long long total, long long n_max, long long nonempty, int P) {
+    if (n_max == 0 || nonempty > P || 2 * nonempty < P) return 0;
+    const long long T = (total + P - 1) / P;
+    return n_max <= T + 2 * kCutTiles ? static_cast<int>(n_max) : 0;
+}
+
 // One pass over the lengths (warp-cooperative): the schedule of this run, its
 // number of units and, for b_at >= 0, the flat unit offset of sequence b_at.
 // Every quantity whose unit depends on the schedule is accumulated for each
 // candidate (tiles; chunks of the plan's size; non-empty sequences, the unit of
 // the one-piece-per-sequence schedule), so one pass serves all three.
-__device__ inline ScheduleScan schedule_scan_warp(const int32_t* seqlens, int B, int L_max, int P, int plan_split,
-                                                  int b_at = -1) {
+template <class Lens>
+__device__ inline ScheduleScan schedule_scan_warp(const Lens& lens, int B, int P, int plan_split, int b_at = -1) {
     const int lane = threadIdx.x & 31;
     long long total = 0, n_max = 0, nonempty = 0, chunks = 0;
     long long at_tiles = 0, at_nonempty = 0, at_chunks = 0;
     for (int b = lane; b < B; b += 32) {
-        const int L = clamp_len(__ldg(seqlens + b), L_max, nullptr);
+        const int L = lens(b);
         const long long n = num_tiles(L);
         const long long c = plan_split > 0 ? num_units(L, plan_split) : 0;
         total += n;
@@ -128,20 +134,19 @@ __device__ inline ScheduleScan schedule_scan_warp(const int32_t* seqlens, int B,
         n_max = y > n_max ? y : n_max;
     }
     if (plan_split > 0) return {plan_split, chunks, at_chunks};
-    if (n_max == 0 || nonempty > P || 2 * nonempty < P) return {0, total, at_tiles};
-    const long long T = (total + P - 1) / P;
-    if (n_max <= T + 2 * kCutTiles) return {static_cast<int>(n_max), nonempty, at_nonempty};
+    const int S = pick_schedule(total, n_max, nonempty, P);
+    if (S > 0) return {S, nonempty, at_nonempty};
     return {0, total, at_tiles};
 }
 
 // Locate the first sequence overlapping flat unit `start` (warp-cooperative).
-__device__ inline void locate_warp(const int32_t* seqlens, int B, int L_max, int S, long long start, int* b_out,
-                                   long long* acc_out) {
+template <class Lens>
+__device__ inline void locate_warp(const Lens& lens, int B, int S, long long start, int* b_out, long long* acc_out) {
     const int lane = threadIdx.x & 31;
     long long acc = 0;
     for (int base = 0; base < B; base += 32) {
         const int b = base + lane;
-        const long long n = (b < B) ? num_units(clamp_len(__ldg(seqlens + b), L_max, nullptr), S) : 0;
+        const long long n = (b < B) ? num_units(lens(b), S) : 0;
         // inclusive prefix within the warp
         long long incl = n;
 #pragma unroll
@@ -176,9 +181,10 @@ struct Piece {
 
 // Sequential walker over the pieces of one partition; every role of a CTA
 // runs its own copy and sees the same sequence of pieces.
-struct PieceWalker {
-    const int32_t* seqlens;
-    int B, L_max, p;
+template <class Lens>
+struct PieceWalkerOf {
+    Lens lens;
+    int B, p;
     int S;                 // 0: balanced schedule over tiles; > 0: chunks of S tiles
     long long start, end;  // flat unit range of this partition
     int b;                 // next sequence to look at
@@ -188,7 +194,7 @@ struct PieceWalker {
     __device__ bool next(Piece& out) {
         if (S > 0) return next_chunk(out);
         while (b < B && acc < end) {
-            const int L = clamp_len(__ldg(seqlens + b), L_max, nullptr);
+            const int L = lens(b);
             const long long n = num_tiles(L);
             const long long lo = acc > start ? acc : start;
             const long long hi = (acc + n) < end ? (acc + n) : end;
@@ -213,7 +219,7 @@ struct PieceWalker {
     // batch-invariant schedule: one S-tile chunk per piece
     __device__ bool next_chunk(Piece& out) {
         while (b < B && acc + k < end) {
-            const int L = clamp_len(__ldg(seqlens + b), L_max, nullptr);
+            const int L = lens(b);
             const long long n = num_tiles(L);
             const long long u = (n + S - 1) / S;
             if (acc + k < start) k = start - acc;
@@ -234,5 +240,6 @@ struct PieceWalker {
         return false;
     }
 };
+using PieceWalker = PieceWalkerOf<SeqLens>;
 
 }  // namespace mla
