@@ -81,7 +81,8 @@ struct Fp8MmaCfg {
     //           pair_full[NP], pair_empty[NP], rope_full[NR], rope_empty[NR]
     static constexpr int kNumBars = 11 + 2 * NP + 2 * NR;
     static constexpr int OFF_MISC = OFF_BAR + kNumBars * 8;
-    static constexpr int kSmemBytes = OFF_MISC + 64 + 1024;
+    static constexpr int OFF_LIST = OFF_MISC + 64;  // paged: the producer's box list
+    static constexpr int kSmemBytes = OFF_LIST + 512 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
     static_assert(OFF_Q % 1024 == 0 && OFF_P % 1024 == 0, "swizzled regions start on 1024-byte boundaries");
     // TMEM: O^T blocks at columns [0, 4 NO), then two S^T buffers (tiles alternate)
@@ -136,7 +137,7 @@ __device__ __forceinline__ int q_row_exponent(float amax) {
 
 // CV: where the cache's rows are (paged.cuh).  In pages, tm_kv's outer
 // dimensions are (row of a page, page) and a chunk is 128 / box boxes stacked in
-// the same layout, each issued by its own lane of the producer warp.
+// the same layout.
 template <int G, class CV = ContigKv>
 __global__ void __launch_bounds__(192, 1)
     mla_decode_fp8mma_kernel(const __grid_constant__ CUtensorMap tm_kv, const MainArgs args,
@@ -249,63 +250,53 @@ __global__ void __launch_bounds__(192, 1)
     if (warp == 4) {
         // ============================================================ TMA producer
         if constexpr (CV::kPaged) {
-            // the whole warp walks; lane l issues box l of each chunk
             uint32_t pair_cnt = 0, rope_cnt = 0;
             int unit = 0;
-            bool ok = true;
-            const bool issues = lane < (kTileKV >> pa.box_log2);
-            const uint32_t dst_off = static_cast<uint32_t>(lane << pa.box_log2) * kChunk;  // a box row is 64 bytes
-            BoxStream<Walker> boxes(pa, walker, issues ? lane << pa.box_log2 : kTileKV);
-            Box ahead = boxes.next();  // the tile prefetched into L2 while the one before it is loaded
-            Box late = boxes.next();   // and the one whose table entry is on its way
-            Piece pc;
-            while (ok && walker.next(pc)) {
-                for (int t = pc.tile_lo; t < pc.tile_hi && ok; ++t) {
-                    const Box box = ahead;
-                    ahead = late;
-                    late = boxes.next();
-                    if (args.prefetch_tiles > 0 && issues && ahead.some && ahead.page >= 0 &&
-                        ahead.page < pa.num_pages)
-                        for (int j = 0; j < kNumChunks; ++j)
-                            ptx::tma_prefetch_3d(&tm_kv, j * kChunk, ahead.row, ahead.page);
-                    const int page = issues ? usable(pa, box, args.status) : 0;
-                    auto arm = [&](uint64_t* full, uint64_t* empty, uint32_t cnt, uint32_t slots, uint32_t bytes) {
-                        ok = ptx::mbar_wait_bounded(empty, ((cnt / slots) & 1) ^ 1, tmo);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) return false;
-                        if (lane == 0) ptx::mbar_arrive_expect_tx(full, bytes);
-                        __syncwarp();
-                        return issues && !(blockIdx.x == 0 && unit == args.stall_unit);
-                    };
-                    {
-                        const uint32_t s = rope_cnt % C::NR;
-                        if (arm(rope_full + s, rope_empty + s, rope_cnt, C::NR, C::kChunkBytes))
-                            ptx::tma_load_3d(rope_smem + s * C::kChunkBytes + dst_off, &tm_kv, rope_full + s,
-                                             (kNumChunks - 1) * kChunk, box.row, page);
-                        if (!ok) break;
-                        ++unit;
-                        ++rope_cnt;
-                    }
-                    for (int pp = 0; pp < 4; ++pp) {
-                        const uint32_t s = pair_cnt % C::NP;
-                        if (arm(pair_full + s, pair_empty + s, pair_cnt, C::NP, C::kPairBytes)) {
-                            uint8_t* dst = pair_smem + s * C::kPairBytes + dst_off;
-                            ptx::tma_load_3d(dst, &tm_kv, pair_full + s, (2 * pp) * kChunk, box.row, page);
-                            ptx::tma_load_3d(dst + C::kChunkBytes, &tm_kv, pair_full + s, (2 * pp + 1) * kChunk,
-                                             box.row, page);
-                        }
-                        if (!ok) break;
-                        ++unit;
-                        ++pair_cnt;
-                    }
+            BoxList<Walker> boxes(pa, walker, smem + C::OFF_LIST, lane, 0, 7);
+            const uint32_t box_bytes = static_cast<uint32_t>(kChunk) << pa.box_log2;  // a box row is 64 bytes
+            const bool ok = boxes.run(args.status, [&](auto count, int tile, bool more) -> bool {
+                constexpr int n_box = decltype(count)::value;
+                int2 box[n_box];
+                if (more && args.prefetch_tiles > 0) {
+                    boxes.template get<n_box>(tile + 1, box);
+                    for (int i = 0; i < n_box; ++i)
+                        for (int j = 0; box[i].x < pa.num_pages && j < kNumChunks; ++j)
+                            ptx::tma_prefetch_3d(&tm_kv, j * kChunk, box[i].y, box[i].x);
                 }
-            }
-            if (!ok && lane == 0) {
-                atomicOr(args.status, kStatusTimeout);
-                *abort_flag = 1;
-            }
+                boxes.template get<n_box>(tile, box);
+                {
+                    const uint32_t s = rope_cnt % C::NR;
+                    if (!ptx::mbar_wait_bounded(rope_empty + s, ((rope_cnt / C::NR) & 1) ^ 1, tmo)) return false;
+                    ptx::mbar_arrive_expect_tx(rope_full + s, C::kChunkBytes);
+                    if (!(blockIdx.x == 0 && unit == args.stall_unit))
+                        for (int i = 0; i < n_box; ++i)
+                            ptx::tma_load_3d(rope_smem + s * C::kChunkBytes + i * box_bytes, &tm_kv, rope_full + s,
+                                             (kNumChunks - 1) * kChunk, box[i].y, box[i].x);
+                    ++unit;
+                    ++rope_cnt;
+                }
+                for (int pp = 0; pp < 4; ++pp) {
+                    const uint32_t s = pair_cnt % C::NP;
+                    if (!ptx::mbar_wait_bounded(pair_empty + s, ((pair_cnt / C::NP) & 1) ^ 1, tmo)) return false;
+                    ptx::mbar_arrive_expect_tx(pair_full + s, C::kPairBytes);
+                    if (!(blockIdx.x == 0 && unit == args.stall_unit))
+                        for (int i = 0; i < n_box; ++i) {
+                            uint8_t* dst = pair_smem + s * C::kPairBytes + i * box_bytes;
+                            ptx::tma_load_3d(dst, &tm_kv, pair_full + s, (2 * pp) * kChunk, box[i].y, box[i].x);
+                            ptx::tma_load_3d(dst + C::kChunkBytes, &tm_kv, pair_full + s, (2 * pp + 1) * kChunk,
+                                             box[i].y, box[i].x);
+                        }
+                    ++unit;
+                    ++pair_cnt;
+                }
+                return true;
+            });
             // drain: every armed load must land before the CTA exits (bounded)
-            if (lane == 0) {
+            if (ptx::elect_one()) {
+                if (!ok) {
+                    atomicOr(args.status, kStatusTimeout);
+                    *abort_flag = 1;
+                }
                 for (uint32_t i = 0; i < C::NP && i < pair_cnt; ++i) {
                     const uint32_t use = pair_cnt - 1 - i;
                     ptx::mbar_wait_bounded(pair_full + (use % C::NP), (use / C::NP) & 1, tmo);
@@ -595,7 +586,12 @@ __global__ void __launch_bounds__(192, 1)
             if (!ok) break;
 
             SeqView view{};
-            if constexpr (CV::kPaged) view = view_of(pa, paged_len(pa, pc.b));
+            int all_lo = 0, all_hi = 0;  // paged: the rows that every query row of the group sees
+            if constexpr (CV::kPaged) {
+                view = view_of(pa, paged_len(pa, pc.b));
+                all_lo = token_rows(pa, view, (g * G + G - 1) >> pa.heads_log2).b0;
+                all_hi = token_rows(pa, view, (g * G) >> pa.heads_log2).b1;
+            }
             float m_ref[G];
             float l_part[G];
 #pragma unroll
@@ -610,6 +606,12 @@ __global__ void __launch_bounds__(192, 1)
                 const int kv_row = row0 + row_in_tile;
                 const bool valid = CV::kPaged || ((kv_row >= t * kTileKV) && (kv_row < pc.L));
 
+                uint32_t hidden = 0;
+                if constexpr (CV::kPaged) {
+                    if (row0 < all_lo || row0 + kTileKV > all_hi)
+                        hidden = hidden_columns(pa, view, G, (g * G) >> pa.heads_log2,
+                                                (g * G) & ((1 << pa.heads_log2) - 1), 1 << pa.heads_log2, kv_row);
+                }
                 const uint32_t sb = tile_cnt & 1;  // S^T and P buffer of this tile
                 ok = ptx::mbar_wait_bounded(s_full + sb, (tile_cnt >> 1) & 1, tmo);
                 if (!ok) break;
@@ -632,9 +634,9 @@ __global__ void __launch_bounds__(192, 1)
                         for (int j = 0; j < 16; ++j) acc[j] += __uint_as_float(r[j]);
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) x[c0 + j] = valid ? acc[j] * qscale[c0 + j] : -INFINITY;
+                    for (int j = 0; j < 16; ++j)
+                        x[c0 + j] = valid && !(hidden >> (c0 + j) & 1) ? acc[j] * qscale[c0 + j] : -INFINITY;
                 }
-                if constexpr (CV::kPaged) mask_columns<G>(pa, view, x, row0, kv_row, g * G, args.H, args.Sq - 1);
                 // column max over the tile's 128 kv rows
                 float* redmax = red + (tile_cnt & 1) * 4 * G;
                 const float wmax = warp_reduce_scatter<G, true>(x, lane);
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(192, 1)
                 for (int j = 0; j < G; ++j) grow |= (tmax[j] > m_ref[j] + C::kLazy);
                 if (first) {
 #pragma unroll
-                    for (int j = 0; j < G; ++j) m_ref[j] = tmax[j];
+                    for (int j = 0; j < G; ++j) m_ref[j] = CV::kPaged ? fmaxf(tmax[j], kNoKey) : tmax[j];
                 } else if (grow) {
                     // O^T must hold the previous tile's PV before it is rescaled (this
                     // tile's PV waits for the P written below)
@@ -670,13 +672,12 @@ __global__ void __launch_bounds__(192, 1)
 #pragma unroll
                     for (int j = 0; j < G; ++j) {
                         const float mn = fmaxf(m_ref[j], tmax[j]);
-                        // paged: a column that has seen no key yet (both -inf) stays as it is
-                        alpha[j] = (CV::kPaged && m_ref[j] == mn) ? 1.f : ex2_approx(m_ref[j] - mn);
+                        alpha[j] = ex2_approx(m_ref[j] - mn);
                         m_ref[j] = mn;
                         l_part[j] *= alpha[j];
                     }
                     // O^T columns of query j (both P terms) *= alpha[j]
-#pragma unroll
+#pragma unroll 1
                     for (int blk = 0; blk < 4; ++blk) {
 #pragma unroll
                         for (int c0 = 0; c0 < C::NO; c0 += 16) {
@@ -698,10 +699,8 @@ __global__ void __launch_bounds__(192, 1)
                 uint32_t w1[G / 4], w2[G / 4];
 #pragma unroll
                 for (int j = 0; j < G; j += 2) {
-                    const float m0 = (CV::kPaged && m_ref[j] == -INFINITY) ? 0.f : m_ref[j];
-                    const float m1 = (CV::kPaged && m_ref[j + 1] == -INFINITY) ? 0.f : m_ref[j + 1];
-                    const float p0 = ex2_approx(x[j] - m0 + C::kPScaleLog2);
-                    const float p1 = ex2_approx(x[j + 1] - m1 + C::kPScaleLog2);
+                    const float p0 = ex2_approx(x[j] - m_ref[j] + C::kPScaleLog2);
+                    const float p1 = ex2_approx(x[j + 1] - m_ref[j + 1] + C::kPScaleLog2);
                     const uint32_t t1 = f32x2_to_e4m3x2(p0, p1);
                     const float2 v1 = e4m3x2_to_f32x2(t1);
                     const uint32_t t2 = f32x2_to_e4m3x2(p0 - v1.x, p1 - v1.y);
@@ -768,10 +767,7 @@ __global__ void __launch_bounds__(192, 1)
                 float lj = (redsum[0 * G + j] + redsum[1 * G + j] + redsum[2 * G + j] + redsum[3 * G + j]) *
                            C::kPScaleInv;
                 float c = 1.f;
-                if (sink_here) {
-                    const float s2 = args.sinks[qr % args.H] * kLog2e;
-                    c = CV::kPaged ? fold_sink_any(mj, lj, s2) : fold_sink(mj, lj, s2);
-                }
+                if (sink_here) c = fold_sink(mj, lj, args.sinks[qr % args.H] * kLog2e);
                 fin[j] = (CV::kPaged && lj == 0.f) ? 0.f : c / lj * args.o_scale * C::kPScaleInv;
                 const float lse_nat = (mj + log2f(lj)) * 0.69314718055994530942f;
                 if (pc.slot < 0)
@@ -781,11 +777,13 @@ __global__ void __launch_bounds__(192, 1)
             }
             ok = group_barrier();
             if (!ok) break;
-#pragma unroll
-            for (int blk = 0; blk < 4; ++blk) {
-                const int dv = blk * 128 + row_in_tile;
-#pragma unroll
-                for (int c0 = 0; c0 < G; c0 += 16) {
+            // rolled: code that runs once a piece is fetched anew each time
+#pragma unroll 1
+            for (int c0 = 0; c0 < G; c0 += 16) {
+#pragma unroll 1
+                for (int blk = 0; blk < 4; ++blk) {
+                    const size_t row0 = static_cast<size_t>(pc.slot < 0 ? pc.b : pc.slot) * args.R + g * G + c0;
+                    const size_t at = row0 * kDv + blk * 128 + row_in_tile;
                     uint32_t r1[16], r2[16];
                     ptx::tmem_ld_16(lane_addr + blk * C::NO + c0, r1);
                     ptx::tmem_ld_16(lane_addr + blk * C::NO + G + c0, r2);
@@ -793,11 +791,10 @@ __global__ void __launch_bounds__(192, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const float o = (__uint_as_float(r1[j]) + __uint_as_float(r2[j])) * fin[c0 + j];
-                        const int qr = g * G + c0 + j;
                         if (pc.slot < 0)
-                            args.out[(static_cast<size_t>(pc.b) * args.R + qr) * kDv + dv] = __float2bfloat16_rn(o);
+                            args.out[at + j * kDv] = __float2bfloat16_rn(o);
                         else
-                            args.part_o[(static_cast<size_t>(pc.slot) * args.R + qr) * kDv + dv] = o;
+                            args.part_o[at + j * kDv] = o;
                     }
                 }
             }

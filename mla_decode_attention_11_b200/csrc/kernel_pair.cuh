@@ -48,9 +48,8 @@
 // barriers (2-SM TMA); MMA completion is multicast to both CTAs.
 // Every wait is bounded; on expiry a CTA records kStatusTimeout and unwinds.
 //
-// The cache in pages (CV = PagedKv, paged.cuh).  The producers' warps walk
-// whole: lane l issues the l-th box of a K chunk (64 / box of them) or V slot
-// (128 / box).  A V slot is then [128 / box][2 chunks][box rows][128 bytes],
+// The cache in pages (CV = PagedKv, paged.cuh).  A K chunk is 64 / box boxes, a
+// V slot 128 / box: a V slot is then [128 / box][2 chunks][box rows][128 bytes],
 // as its boxes land; each 16-row step of the PV MMAs lies in one box, so only
 // the descriptors' offsets differ.  In a tile with rows that no token sees, the
 // softmax threads clear those rows of V: the PV issuer waits for the tile's V
@@ -91,7 +90,8 @@ struct PairCfg {
     // and v_here: paged, the V slots of a tile with rows to clear have landed
     static constexpr int kNumBars = 7 + NP + 3 * NS + 2 * NK + 2 * NV;
     static constexpr int OFF_MISC = OFF_BAR + kNumBars * 8;
-    static constexpr int kSmemBytes = OFF_MISC + 64;
+    static constexpr int OFF_LIST = OFF_MISC + 64;             // paged: box lists of the K and the V producer
+    static constexpr int kSmemBytes = OFF_LIST + 2 * 512;
     static constexpr uint32_t kTmemCols = 512;                 // O: [0,256), S buffers from 256, 64 each
     static constexpr uint32_t kColS = 256;
     static_assert(NS >= 2 && 256 + 64 * NS <= 512, "S buffers must fit next to O in TMEM");
@@ -243,53 +243,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         // ============================================================ Q + K producer
         if constexpr (CV::kPaged) {
             uint32_t k_cnt = 0, piece_cnt = 0;
-            int unit = 0;
-            bool ok = true;
-            const bool issues = lane < (64 >> pa.box_log2);  // the boxes of this CTA's 64 rows of a tile
-            const int off = lane << pa.box_log2;
-            BoxStream<Walker> boxes(pa, walker, issues ? static_cast<int>(rank) * 64 + off : kTileKV);
-            Box cur = boxes.next(), ahead = cur;  // the tile loaded, the tile prefetched into L2
-            Box late = boxes.next();              // and the one whose table entry is on its way
+            int unit = 0, t = 0;
             Piece pc;
-            bool started = false;
-            while (ok && walker.next(pc)) {
-                if (piece_cnt > 0) ok = ptx::mbar_wait_bounded(q_empty, (piece_cnt - 1) & 1, tmo);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (lane == 0) {
+            bool open = false;  // tiles of pc are left
+            // the boxes of this CTA's 64 rows of a tile
+            BoxList<Walker> boxes(pa, walker, smem + C::OFF_LIST, lane, static_cast<int>(rank) * 64, 6);
+            const uint32_t box_bytes = 128u << pa.box_log2;
+            const bool ok = boxes.run(args.status, [&](auto count, int tile, bool more) -> bool {
+                constexpr int n_box = decltype(count)::value;
+                int2 box[n_box];
+                if (!open) {
+                    walker.next(pc);
+                    t = pc.tile_lo;
+                    open = true;
+                    if (piece_cnt > 0 && !ptx::mbar_wait_bounded(q_empty, (piece_cnt - 1) & 1, tmo)) return false;
                     if (leader) ptx::mbar_arrive_expect_tx(q_full, 2 * kNumChunks * C::kQChunk);
                     const int qrow = pc.b * args.R + g * 128 + static_cast<int>(rank) * 64;
                     if (!(stall_cta && unit == args.stall_unit))
                         ptx::tma_load_3d_pair(q_smem, &tm_q, lead_q_full, 0, qrow, 0);
+                    ++unit;
+                    ++piece_cnt;
                 }
-                ++unit;
-                for (int t = pc.tile_lo; t < pc.tile_hi && ok; ++t) {
-                    if (started) cur = ahead;
-                    started = true;
-                    ahead = late;
-                    late = boxes.next();
-                    if (args.prefetch_tiles > 0 && issues && ahead.some && ahead.page >= 0 && ahead.page < pa.num_pages)
-                        ptx::tma_prefetch_4d(&tm_pf, 0, ahead.row, 0, ahead.page);
-                    const int page = issues ? usable(pa, cur, args.status) : 0;
-                    for (int jj = 0; jj < kNumChunks; ++jj) {
-                        const int j = (jj == 0) ? 8 : jj - 1;  // rope chunk first
-                        const uint32_t s = k_cnt % NK;
-                        ok = ptx::mbar_wait_bounded(k_empty + s, ((k_cnt / NK) & 1) ^ 1, tmo);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        if (leader && lane == 0) ptx::mbar_arrive_expect_tx(k_full + s, 2 * C::kKChunk);
-                        __syncwarp();
-                        if (issues && !(stall_cta && unit == args.stall_unit))
-                            ptx::tma_load_3d_pair(k_smem + s * C::kKChunk + off * 128, &tm_k,
-                                                  ptx::mapa_shared(ptx::smem_u32(k_full + s), 0), j * kChunk, cur.row,
-                                                  page);
-                        ++unit;
-                        ++k_cnt;
-                    }
+                if (more && args.prefetch_tiles > 0) {  // the next tile into L2, K and V columns alike
+                    boxes.template get<n_box>(tile + 1, box);
+                    for (int i = 0; i < n_box; ++i)
+                        if (box[i].x < pa.num_pages) ptx::tma_prefetch_4d(&tm_pf, 0, box[i].y, 0, box[i].x);
                 }
-                ++piece_cnt;
-            }
-            if (lane == 0) {
+                boxes.template get<n_box>(tile, box);
+                for (int jj = 0; jj < kNumChunks; ++jj) {
+                    const int j = (jj == 0) ? 8 : jj - 1;  // rope chunk first
+                    const uint32_t s = k_cnt % NK;
+                    if (!ptx::mbar_wait_bounded(k_empty + s, ((k_cnt / NK) & 1) ^ 1, tmo)) return false;
+                    if (leader) ptx::mbar_arrive_expect_tx(k_full + s, 2 * C::kKChunk);
+                    if (!(stall_cta && unit == args.stall_unit))
+                        for (int i = 0; i < n_box; ++i)
+                            ptx::tma_load_3d_pair(k_smem + s * C::kKChunk + i * box_bytes, &tm_k,
+                                                  ptx::mapa_shared(ptx::smem_u32(k_full + s), 0), j * kChunk, box[i].y,
+                                                  box[i].x);
+                    ++unit;
+                    ++k_cnt;
+                }
+                if (++t == pc.tile_hi) open = false;
+                return true;
+            });
+            if (ptx::elect_one()) {
                 if (!ok) atomicOr(args.status, kStatusTimeout);
                 if (leader) {  // every armed load has landed before teardown
                     bool drained = true;
@@ -393,34 +390,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         // ============================================================ V producer
         if constexpr (CV::kPaged) {
             uint32_t v_cnt = 0;
-            bool ok = true;
-            const bool issues = lane < (kTileKV >> pa.box_log2);
-            const int off = lane << pa.box_log2;
-            BoxStream<Walker> boxes(pa, walker, issues ? off : kTileKV);
-            Box ahead = boxes.next();
-            Piece pc;
-            while (ok && walker.next(pc)) {
-                for (int t = pc.tile_lo; t < pc.tile_hi && ok; ++t) {
-                    const Box cur = ahead;
-                    ahead = boxes.next();
-                    const int page = issues ? usable(pa, cur, args.status) : 0;
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t s = v_cnt % NV;
-                        ok = ptx::mbar_wait_bounded(v_empty + s, ((v_cnt / NV) & 1) ^ 1, tmo);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        if (leader && lane == 0) ptx::mbar_arrive_expect_tx(v_full + s, 2 * C::kVSlot);
-                        __syncwarp();
-                        const int col0 = 256 * i + 128 * static_cast<int>(rank);  // two adjacent chunks, one box
-                        if (issues)
-                            ptx::tma_load_4d_pair(v_smem + s * C::kVSlot + off * 256, &tm_v,
-                                                  ptx::mapa_shared(ptx::smem_u32(v_full + s), 0), 0, cur.row,
-                                                  col0 / kChunk, page);
-                        ++v_cnt;
-                    }
+            BoxList<Walker> boxes(pa, walker, smem + C::OFF_LIST + 512, lane, 0, 7);
+            const uint32_t box_bytes = 256u << pa.box_log2;  // two chunks
+            const bool ok = boxes.run(args.status, [&](auto count, int tile, bool) -> bool {
+                constexpr int n_box = decltype(count)::value;
+                int2 box[n_box];
+                boxes.template get<n_box>(tile, box);
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t s = v_cnt % NV;
+                    if (!ptx::mbar_wait_bounded(v_empty + s, ((v_cnt / NV) & 1) ^ 1, tmo)) return false;
+                    if (leader) ptx::mbar_arrive_expect_tx(v_full + s, 2 * C::kVSlot);
+                    const int col0 = 256 * i + 128 * static_cast<int>(rank);  // two adjacent chunks, one box
+                    for (int k = 0; k < n_box; ++k)
+                        ptx::tma_load_4d_pair(v_smem + s * C::kVSlot + k * box_bytes, &tm_v,
+                                              ptx::mapa_shared(ptx::smem_u32(v_full + s), 0), 0, box[k].y,
+                                              col0 / kChunk, box[k].x);
+                    ++v_cnt;
                 }
-            }
-            if (lane == 0) {
+                return true;
+            });
+            if (ptx::elect_one()) {
                 if (!ok) atomicOr(args.status, kStatusTimeout);
                 if (leader) {
                     bool drained = true;
@@ -633,7 +622,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             RowRange seen{};          // paged: the rows this thread's query row sees
             if constexpr (CV::kPaged) {
                 view = view_of(pa, paged_len(pa, pc.b));
-                seen = token_rows(pa, view, (g * 128 + static_cast<int>(rank) * 64 + r) / pa.mask_rows);
+                seen = token_rows(pa, view, (g * 128 + static_cast<int>(rank) * 64 + r) >> pa.heads_log2);
             }
             for (int t = pc.tile_lo; t < pc.tile_hi; ++t) {
                 const bool first = (t == pc.tile_lo);
@@ -667,9 +656,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 // previous tile (below lo); every key of a tile is below L
                 if constexpr (CV::kPaged) {
                     if (!seen.all(kv0, 64)) {
+                        const uint64_t bits = bits_between(0, seen.f - kv0) | bits_between(seen.b0 - kv0, seen.b1 - kv0);
+                        const uint32_t lo32 = static_cast<uint32_t>(bits), hi32 = static_cast<uint32_t>(bits >> 32);
 #pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            if (!seen.sees(kv0 + j)) x[j] = -INFINITY;
+                        for (int j = 0; j < 32; ++j) {
+                            if (!(lo32 >> j & 1)) x[j] = -INFINITY;
+                            if (!(hi32 >> j & 1)) x[32 + j] = -INFINITY;
+                        }
                     }
                 } else if (row0 < lo) {
 #pragma unroll
@@ -689,9 +682,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 // the row max outgrew the reference by more than 8 (p <= 2^8).
                 uint32_t packed[32];
                 float lsum = 0.f;
-                auto exps = [&](float m_at) {
-                    // paged: a row that has seen no key yet (its scores all -inf)
-                    const float m = (CV::kPaged && m_at == -INFINITY) ? 0.f : m_at;
+                auto exps = [&](float m) {
                     // the exponents and the row sum two lanes at a time (packed fp32)
                     float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
@@ -714,7 +705,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 float alpha = 1.f;
                 bool grow = false;
                 if (first) {
-                    m_ref = mrow;
+                    m_ref = CV::kPaged ? fmaxf(mrow, kNoKey) : mrow;
                     exps(m_ref);
                 } else if (mrow > m_ref + 8.f) {
                     grow = true;
@@ -807,10 +798,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 if (slot < 0 && pa.whole_slot >= 0) slot = pa.whole_slot + pc.b;
             // a sink applies once per row: to whole sequences here, to cut ones in the combine
             float o_fac = 1.f;
-            if (args.sinks != nullptr && slot < 0) {
-                const float s2 = args.sinks[qrow % args.H] * kLog2e;
-                o_fac = CV::kPaged ? fold_sink_any(m_ref, l_row, s2) : fold_sink(m_ref, l_row, s2);
-            }
+            if (args.sinks != nullptr && slot < 0) o_fac = fold_sink(m_ref, l_row, args.sinks[qrow % args.H] * kLog2e);
             const float inv_l = (CV::kPaged && l_row == 0.f) ? 0.f : o_fac / l_row;
             if (h == 0) {
                 const float lse_nat = (m_ref + log2f(l_row)) * 0.69314718055994530942f;

@@ -116,12 +116,6 @@ __device__ __forceinline__ float fold_sink(float& m, float& l, float s2) {
     return c;
 }
 
-// fold_sink for rows that may have no keys at all (m = -inf, l = 0): those keep
-// l = 0 when there is no sink either.
-__device__ __forceinline__ float fold_sink_any(float& m, float& l, float s2) {
-    return fmaxf(m, s2) == -INFINITY ? 1.f : fold_sink(m, l, s2);
-}
-
 constexpr float kLog2e = 1.4426950408889634074f;
 
 // FP8 cache at G = 16: operand pair slots and 8-KB staging slots (5 + 3 fill
@@ -162,7 +156,10 @@ struct TransposedCfg {
     //           pair_empty[NP], rope_full[NR], rope_empty[NR], f8_full[NF], f8_empty[NF], q_ready
     static constexpr int kNumBars = 7 + 2 * NP + 2 * NR + 2 * NF + (SH::kFp8 ? 1 : 0);
     static constexpr int OFF_MISC = OFF_BAR + kNumBars * 8;
-    static constexpr int kSmemBytes = OFF_MISC + 64 + 1024;  // + slack to align the base to 1024
+    // paged: the producer's box list (in the rope slot, which MHA does not use, where there is no room)
+    static constexpr int kListBytes = SH::kFp8 || SH::kMha ? 0 : 512;
+    static constexpr int OFF_LIST = SH::kMha ? OFF_ROPE : OFF_MISC + 64;
+    static constexpr int kSmemBytes = OFF_MISC + 64 + kListBytes + 1024;  // + slack to align the base to 1024
     static_assert(kSmemBytes <= 232448, "shared memory budget");
     // TMEM: O^T blocks at columns [0, kDvBlocks G), S^T after them
     static constexpr int kCols = (SH::kDvBlocks + 1) * G;
@@ -308,8 +305,7 @@ __device__ __forceinline__ int group_row(const MainArgs& a, int G, int g, int j)
 //
 // CV: where the kv rows are (paged.cuh).  In pages, the maps' outer dimensions
 // are (row of a page, page), a tile is 128 / box boxes stacked in the same
-// layout, each issued by its own lane of the producer warp, and the rows a
-// query row sees depend on its token.
+// layout, and the rows a query row sees depend on its token.
 template <int G, class SH = MlaShape, class CV = ContigKv>
 __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
     mla_decode_transposed_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
@@ -444,23 +440,21 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
     if (warp == 4) {
         // ============================================================ TMA producer
         if constexpr (CV::kPaged) {
-            // the whole warp walks; lane l issues box l of each tile, lane 0 Q
             uint32_t pair_cnt = 0, rope_cnt = 0, piece_cnt = 0;
-            int unit = 0;
-            bool ok = true;
-            const bool issues = lane < (kTileKV >> pa.box_log2);
-            const uint32_t dst_off = static_cast<uint32_t>(lane << pa.box_log2) * 128;  // a box row is 128 bytes
-            BoxStream<Walker> boxes(pa, walker, issues ? lane << pa.box_log2 : kTileKV);
-            Box ahead = boxes.next();  // the table entry of the next tile is on its way while a tile is issued
+            int unit = 0, t = 0;
             Piece pc;
-            while (ok && walker.next(pc)) {
-                if (piece_cnt > 0) ok = ptx::mbar_wait_bounded(q_empty, (piece_cnt - 1) & 1, tmo);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    const bool skip = blockIdx.x == 0 && unit == args.stall_unit;
+            bool open = false;  // tiles of pc are left
+            BoxList<Walker> boxes(pa, walker, smem + C::OFF_LIST, lane, 0, 7);
+            const uint32_t box_bytes = 128u << pa.box_log2;  // a box row is 128 bytes
+            const bool ok = boxes.run(args.status, [&](auto count, int tile, bool) -> bool {
+                constexpr int n_box = decltype(count)::value;
+                const bool may_stall = blockIdx.x == 0;
+                if (!open) {
+                    walker.next(pc);
+                    t = pc.tile_lo;
+                    open = true;
+                    if (piece_cnt > 0 && !ptx::mbar_wait_bounded(q_empty, (piece_cnt - 1) & 1, tmo)) return false;
+                    const bool skip = may_stall && unit == args.stall_unit;
                     if constexpr (SH::kMha) {
                         const int gq = args.H / args.Hkv;
                         ptx::mbar_arrive_expect_tx(q_full, SH::kQKChunks * args.Sq * gq * 128);
@@ -475,56 +469,52 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                                 ptx::tma_load_2d(q_smem + c * C::kQChunkBytes, &tm_q, q_full, c * kChunk,
                                                  pc.b * args.R + g * G);
                     }
+                    ++unit;
+                    ++piece_cnt;
                 }
-                ++unit;
-                for (int t = pc.tile_lo; t < pc.tile_hi && ok; ++t) {
-                    const Box box = ahead;
-                    ahead = boxes.next();
-                    const int page = issues ? usable(pa, box, args.status) : 0;
-                    auto arm = [&](uint64_t* full, uint64_t* empty, uint32_t cnt, uint32_t slots, uint32_t bytes) {
-                        ok = ptx::mbar_wait_bounded(empty, ((cnt / slots) & 1) ^ 1, tmo);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) return false;
-                        if (lane == 0) ptx::mbar_arrive_expect_tx(full, bytes);
-                        __syncwarp();
-                        return issues && !(blockIdx.x == 0 && unit == args.stall_unit);
-                    };
-                    if constexpr (!SH::kMha) {
-                        const uint32_t s = rope_cnt % C::NR;
-                        if (arm(rope_full + s, rope_empty + s, rope_cnt, C::NR, C::kChunkBytes))
-                            ptx::tma_load_3d(rope_smem + s * C::kChunkBytes + dst_off, &tm_kv, rope_full + s,
-                                             8 * kChunk, box.row, page);
-                        if (!ok) break;
-                        ++unit;
-                        ++rope_cnt;
-                    }
-                    for (int pp = 0; pp < (SH::kMha ? 2 : 4); ++pp) {
-                        const uint32_t s = pair_cnt % C::NP;
-                        if (arm(pair_full + s, pair_empty + s, pair_cnt, C::NP, C::kPairBytes)) {
-                            uint8_t* dst = pair_smem + s * C::kPairBytes + dst_off;
+                int2 box[n_box];
+                boxes.template get<n_box>(tile, box);
+                if constexpr (!SH::kMha) {
+                    const uint32_t s = rope_cnt % C::NR;
+                    if (!ptx::mbar_wait_bounded(rope_empty + s, ((rope_cnt / C::NR) & 1) ^ 1, tmo)) return false;
+                    ptx::mbar_arrive_expect_tx(rope_full + s, C::kChunkBytes);
+                    if (!(may_stall && unit == args.stall_unit))
+                        for (int i = 0; i < n_box; ++i)
+                            ptx::tma_load_3d(rope_smem + s * C::kChunkBytes + i * box_bytes, &tm_kv, rope_full + s,
+                                             8 * kChunk, box[i].y, box[i].x);
+                    ++unit;
+                    ++rope_cnt;
+                }
+                for (int pp = 0; pp < (SH::kMha ? 2 : 4); ++pp) {
+                    const uint32_t s = pair_cnt % C::NP;
+                    if (!ptx::mbar_wait_bounded(pair_empty + s, ((pair_cnt / C::NP) & 1) ^ 1, tmo)) return false;
+                    ptx::mbar_arrive_expect_tx(pair_full + s, C::kPairBytes);
+                    if (!(may_stall && unit == args.stall_unit))
+                        for (int i = 0; i < n_box; ++i) {
+                            uint8_t* dst = pair_smem + s * C::kPairBytes + i * box_bytes;
+                            const int row = box[i].y, page = box[i].x;
                             if constexpr (SH::kMha) {  // the tile's K rows, then its V rows (kv head g)
                                 const CUtensorMap* tm = (pp == 0) ? &tm_kv : &tm_v;
-                                ptx::tma_load_4d(dst, tm, pair_full + s, 0, g, box.row, page);
-                                ptx::tma_load_4d(dst + C::kChunkBytes, tm, pair_full + s, kChunk, g, box.row, page);
+                                ptx::tma_load_4d(dst, tm, pair_full + s, 0, g, row, page);
+                                ptx::tma_load_4d(dst + C::kChunkBytes, tm, pair_full + s, kChunk, g, row, page);
                             } else {
-                                ptx::tma_load_3d(dst, &tm_kv, pair_full + s, (2 * pp) * kChunk, box.row, page);
+                                ptx::tma_load_3d(dst, &tm_kv, pair_full + s, (2 * pp) * kChunk, row, page);
                                 ptx::tma_load_3d(dst + C::kChunkBytes, &tm_kv, pair_full + s, (2 * pp + 1) * kChunk,
-                                                 box.row, page);
+                                                 row, page);
                             }
                         }
-                        if (!ok) break;
-                        ++unit;
-                        ++pair_cnt;
-                    }
+                    ++unit;
+                    ++pair_cnt;
                 }
-                ++piece_cnt;
-            }
-            if (!ok && lane == 0) {
-                atomicOr(args.status, kStatusTimeout);
-                *abort_flag = 1;
-            }
+                if (++t == pc.tile_hi) open = false;
+                return true;
+            });
             // drain: every armed load must have landed before the CTA can exit (bounded)
-            if (lane == 0) {
+            if (ptx::elect_one()) {
+                if (!ok) {
+                    atomicOr(args.status, kStatusTimeout);
+                    *abort_flag = 1;
+                }
                 if (piece_cnt > 0) ptx::mbar_wait_bounded(q_full, (piece_cnt - 1) & 1, tmo);
                 for (uint32_t i = 0; i < C::NP && i < pair_cnt; ++i) {
                     const uint32_t use = pair_cnt - 1 - i;
@@ -837,7 +827,13 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
         Piece pc;
         while (ok && walker.next(pc)) {
             SeqView view{};
-            if constexpr (CV::kPaged) view = view_of(pa, paged_len(pa, pc.b));
+            int all_lo = 0, all_hi = 0;  // paged: the rows that every query row of the group sees
+            if constexpr (CV::kPaged) {
+                view = view_of(pa, paged_len(pa, pc.b));
+                const int last = SH::kMha ? pa.Sq - 1 : (g * G + G - 1) >> pa.heads_log2;
+                all_lo = token_rows(pa, view, last).b0;
+                all_hi = token_rows(pa, view, SH::kMha ? 0 : (g * G) >> pa.heads_log2).b1;
+            }
             float m_ref[G];
             float l_part[G];
 #pragma unroll
@@ -852,6 +848,14 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                 const int kv_row = row0 + row_in_tile;
                 const bool valid = CV::kPaged || ((kv_row >= t * kTileKV) && (kv_row < pc.L));
 
+                uint32_t hidden = 0;
+                if constexpr (CV::kPaged) {
+                    const int r0 = SH::kMha ? 0 : g * G;
+                    if (row0 < all_lo || row0 + kTileKV > all_hi)
+                        hidden = hidden_columns(pa, view, G, SH::kMha ? 0 : r0 >> pa.heads_log2,
+                                                SH::kMha ? 0 : r0 & ((1 << pa.heads_log2) - 1),
+                                                SH::kMha ? args.H / args.Hkv : 1 << pa.heads_log2, kv_row);
+                }
                 ok = ptx::mbar_wait_bounded(s_full, tile_cnt & 1, tmo);
                 if (!ok) break;
                 ptx::tc_fence_after();
@@ -864,12 +868,10 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                         ptx::tmem_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            x[c0 + j] = valid ? __uint_as_float(r[j]) * args.scale_log2 : -INFINITY;
+                            x[c0 + j] = valid && !(hidden >> (c0 + j) & 1) ? __uint_as_float(r[j]) * args.scale_log2
+                                                                          : -INFINITY;
                     }
                 }
-                if constexpr (CV::kPaged)
-                    mask_columns<G>(pa, view, x, row0, kv_row, SH::kMha ? 0 : g * G,
-                                    SH::kMha ? args.H / args.Hkv : args.H, args.Sq - 1);
                 // column max over the tile's 128 kv rows
                 float* redmax = red + (tile_cnt & 1) * 4 * G;
                 const float wmax = warp_reduce_scatter<G, true>(x, lane);
@@ -896,20 +898,19 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                 for (int j = 0; j < G; ++j) grow |= (tmax[j] > m_ref[j] + 8.f);
                 if (first) {
 #pragma unroll
-                    for (int j = 0; j < G; ++j) m_ref[j] = tmax[j];
+                    for (int j = 0; j < G; ++j) m_ref[j] = CV::kPaged ? fmaxf(tmax[j], kNoKey) : tmax[j];
                 } else if (grow) {
                     float alpha[G];
 #pragma unroll
                     for (int j = 0; j < G; ++j) {
                         const float mn = fmaxf(m_ref[j], tmax[j]);
-                        // paged: a column that has seen no key yet (both -inf) stays as it is
-                        alpha[j] = (CV::kPaged && m_ref[j] == mn) ? 1.f : ex2_approx(m_ref[j] - mn);
+                        alpha[j] = ex2_approx(m_ref[j] - mn);
                         m_ref[j] = mn;
                         l_part[j] *= alpha[j];
                     }
                     // O^T columns j *= alpha[j]; PV of the previous tile has
                     // completed (it was committed before this tile's S^T).
-#pragma unroll
+#pragma unroll 1
                     for (int blk = 0; blk < SH::kDvBlocks; ++blk) {
 #pragma unroll
                         for (int c0 = 0; c0 < G; c0 += 16) {
@@ -927,10 +928,8 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                 uint32_t packed[G / 2];
 #pragma unroll
                 for (int j = 0; j < G; j += 2) {
-                    const float m0 = (CV::kPaged && m_ref[j] == -INFINITY) ? 0.f : m_ref[j];
-                    const float m1 = (CV::kPaged && m_ref[j + 1] == -INFINITY) ? 0.f : m_ref[j + 1];
-                    const float p0 = ex2_approx(x[j] - m0);
-                    const float p1 = ex2_approx(x[j + 1] - m1);
+                    const float p0 = ex2_approx(x[j] - m_ref[j]);
+                    const float p1 = ex2_approx(x[j + 1] - m_ref[j + 1]);
                     l_part[j] += p0;
                     l_part[j + 1] += p1;
                     if constexpr (SH::kFp8) {
@@ -1007,10 +1006,7 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                     if (jj == j) mj = m_ref[jj];
                 float lj = redsum[0 * G + j] + redsum[1 * G + j] + redsum[2 * G + j] + redsum[3 * G + j];
                 float c = 1.f;
-                if (sink_here) {
-                    const float s2 = args.sinks[qr % args.H] * kLog2e;
-                    c = CV::kPaged ? fold_sink_any(mj, lj, s2) : fold_sink(mj, lj, s2);
-                }
+                if (sink_here) c = fold_sink(mj, lj, args.sinks[qr % args.H] * kLog2e);
                 fin[j] = (CV::kPaged && lj == 0.f) ? 0.f : c / lj * args.o_scale;
                 const float lse_nat = (mj + log2f(lj)) * 0.69314718055994530942f;
                 if (slot < 0)
@@ -1020,28 +1016,32 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
             }
             ok = group_barrier();
             if (!ok) break;
-#pragma unroll
-            for (int blk = 0; blk < SH::kDvBlocks; ++blk) {
-                const int dv = blk * 128 + row_in_tile;
-#pragma unroll
-                for (int c0 = 0; c0 < G; c0 += 16) {
+            // rolled: code that runs once a piece is fetched anew each time (unrolled
+            // over all columns and blocks, 6 us of a G = 32 piece went into it)
+#pragma unroll 1
+            for (int c0 = 0; c0 < G; c0 += 16) {
+#pragma unroll 1
+                for (int blk = 0; blk < SH::kDvBlocks; ++blk) {
+                    const int dv = blk * 128 + row_in_tile;
+                    const size_t row0 = static_cast<size_t>(slot < 0 ? pc.b : slot) * args.R + group_row<SH>(args, G, g, c0);
+                    int rem = SH::kMha ? c0 % (args.H / args.Hkv) : 0;  // MHA: column within its token's
+                    size_t at = row0 * SH::kDv + dv;
                     uint32_t r[16];
                     ptx::tmem_ld_16(lane_addr + blk * G + c0, r);
                     ptx::tmem_wait_ld();
-                    if (slot < 0) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if (c0 + j >= n_cols) continue;
-                            const size_t orow = static_cast<size_t>(pc.b) * args.R + group_row<SH>(args, G, g, c0 + j);
-                            args.out[orow * SH::kDv + dv] = __float2bfloat16_rn(__uint_as_float(r[j]) * fin[c0 + j]);
+                    for (int j = 0; j < 16; ++j) {
+                        if (!SH::kMha || c0 + j < n_cols) {
+                            const float o = __uint_as_float(r[j]) * fin[c0 + j];
+                            if (slot < 0)
+                                args.out[at] = __float2bfloat16_rn(o);
+                            else
+                                args.part_o[at] = o;
                         }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if (c0 + j >= n_cols) continue;
-                            const size_t orow =
-                                static_cast<size_t>(slot) * args.R + group_row<SH>(args, G, g, c0 + j);
-                            args.part_o[orow * SH::kDv + dv] = __uint_as_float(r[j]) * fin[c0 + j];
+                        at += SH::kDv;
+                        if (SH::kMha && ++rem == args.H / args.Hkv) {  // the next token's heads
+                            rem = 0;
+                            at += static_cast<size_t>(args.H - args.H / args.Hkv) * SH::kDv;
                         }
                     }
                 }

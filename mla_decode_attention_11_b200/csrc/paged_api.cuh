@@ -67,13 +67,19 @@ mla::PagedArgs paged_args(const mla_plan& pl, const int32_t* seqlens, const int3
     a.L_max = pl.L_max;
     a.num_pages = num_pages;
     a.page_size = pl.page_size;
+    // positions n < 2^25: with 2^s >= page_size > 2^(s-1) and mul = ceil(2^(25+s) / page_size), n * (mul * page_size -
+    // 2^(25+s)) < 2^25 * page_size <= 2^(25+s), so n * mul >> (25+s) is exact; mul < 2^27
+    int s = 0;
+    while ((1 << s) < pl.page_size) ++s;
+    a.page_shift = 25 + s;
+    a.page_mul = static_cast<uint32_t>(((1ull << a.page_shift) + pl.page_size - 1) / pl.page_size);
     a.box = page_box(pl.page_size, pair ? 64 : 128);
     a.box_log2 = box_log2(a.box);
     a.Sq = pl.Sq;
     // a window that no sequence can fill leaves nothing out
     a.window = pl.window >= pl.L_max ? 0 : pl.window;
     a.first = pl.first_tokens < pl.L_max ? pl.first_tokens : pl.L_max;
-    a.mask_rows = pl.H / pl.Hkv;
+    while ((1 << a.heads_log2) < pl.H) ++a.heads_log2;
     a.whole_slot = -1;
     return a;
 }
