@@ -252,40 +252,38 @@ __global__ void __launch_bounds__(192, 1)
         if constexpr (CV::kPaged) {
             uint32_t pair_cnt = 0, rope_cnt = 0;
             int unit = 0;
-            BoxList<Walker> boxes(pa, walker, smem + C::OFF_LIST, lane, 0, 7);
+            BoxList<Walker, 8> boxes(pa, walker, smem + C::OFF_LIST, lane, 0, 7);
             const uint32_t box_bytes = static_cast<uint32_t>(kChunk) << pa.box_log2;  // a box row is 64 bytes
-            const bool ok = boxes.run(args.status, [&](auto count, int tile, bool more) -> bool {
-                constexpr int n_box = decltype(count)::value;
-                int2 box[n_box];
-                if (more && args.prefetch_tiles > 0) {
-                    boxes.template get<n_box>(tile + 1, box);
-                    for (int i = 0; i < n_box; ++i)
-                        for (int j = 0; box[i].x < pa.num_pages && j < kNumChunks; ++j)
-                            ptx::tma_prefetch_3d(&tm_kv, j * kChunk, box[i].y, box[i].x);
-                }
-                boxes.template get<n_box>(tile, box);
+            const bool ok = boxes.run(args.status, [&](int tile, bool more) -> bool {
+                if (more && args.prefetch_tiles > 0)  // the next tile
+                    boxes.get(tile + 1).each([&](int, int row, int page) {
+                        if (page < pa.num_pages) ptx::tma_prefetch_4d(&pa.prefetch, 0, row, 0, page);
+                    });
+                const auto box = boxes.get(tile);
                 {
                     const uint32_t s = rope_cnt % C::NR;
                     if (!ptx::mbar_wait_bounded(rope_empty + s, ((rope_cnt / C::NR) & 1) ^ 1, tmo)) return false;
                     ptx::mbar_arrive_expect_tx(rope_full + s, C::kChunkBytes);
                     if (!(blockIdx.x == 0 && unit == args.stall_unit))
-                        for (int i = 0; i < n_box; ++i)
+                        box.each([&](int i, int row, int page) {
                             ptx::tma_load_3d(rope_smem + s * C::kChunkBytes + i * box_bytes, &tm_kv, rope_full + s,
-                                             (kNumChunks - 1) * kChunk, box[i].y, box[i].x);
+                                             (kNumChunks - 1) * kChunk, row, page);
+                        });
                     ++unit;
                     ++rope_cnt;
                 }
+#pragma unroll 1
                 for (int pp = 0; pp < 4; ++pp) {
                     const uint32_t s = pair_cnt % C::NP;
                     if (!ptx::mbar_wait_bounded(pair_empty + s, ((pair_cnt / C::NP) & 1) ^ 1, tmo)) return false;
                     ptx::mbar_arrive_expect_tx(pair_full + s, C::kPairBytes);
                     if (!(blockIdx.x == 0 && unit == args.stall_unit))
-                        for (int i = 0; i < n_box; ++i) {
+                        box.each([&](int i, int row, int page) {
                             uint8_t* dst = pair_smem + s * C::kPairBytes + i * box_bytes;
-                            ptx::tma_load_3d(dst, &tm_kv, pair_full + s, (2 * pp) * kChunk, box[i].y, box[i].x);
-                            ptx::tma_load_3d(dst + C::kChunkBytes, &tm_kv, pair_full + s, (2 * pp + 1) * kChunk,
-                                             box[i].y, box[i].x);
-                        }
+                            ptx::tma_load_3d(dst, &tm_kv, pair_full + s, (2 * pp) * kChunk, row, page);
+                            ptx::tma_load_3d(dst + C::kChunkBytes, &tm_kv, pair_full + s, (2 * pp + 1) * kChunk, row,
+                                             page);
+                        });
                     ++unit;
                     ++pair_cnt;
                 }

@@ -247,11 +247,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             Piece pc;
             bool open = false;  // tiles of pc are left
             // the boxes of this CTA's 64 rows of a tile
-            BoxList<Walker> boxes(pa, walker, smem + C::OFF_LIST, lane, static_cast<int>(rank) * 64, 6);
+            BoxList<Walker, 4> boxes(pa, walker, smem + C::OFF_LIST, lane, static_cast<int>(rank) * 64, 6);
             const uint32_t box_bytes = 128u << pa.box_log2;
-            const bool ok = boxes.run(args.status, [&](auto count, int tile, bool more) -> bool {
-                constexpr int n_box = decltype(count)::value;
-                int2 box[n_box];
+            const bool ok = boxes.run(args.status, [&](int tile, bool more) -> bool {
                 if (!open) {
                     walker.next(pc);
                     t = pc.tile_lo;
@@ -264,22 +262,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                     ++unit;
                     ++piece_cnt;
                 }
-                if (more && args.prefetch_tiles > 0) {  // the next tile into L2, K and V columns alike
-                    boxes.template get<n_box>(tile + 1, box);
-                    for (int i = 0; i < n_box; ++i)
-                        if (box[i].x < pa.num_pages) ptx::tma_prefetch_4d(&tm_pf, 0, box[i].y, 0, box[i].x);
-                }
-                boxes.template get<n_box>(tile, box);
+                if (more && args.prefetch_tiles > 0)  // the next tile into L2, K and V columns alike
+                    boxes.get(tile + 1).each([&](int, int row, int page) {
+                        if (page < pa.num_pages) ptx::tma_prefetch_4d(&tm_pf, 0, row, 0, page);
+                    });
+                const auto box = boxes.get(tile);
+#pragma unroll 3
                 for (int jj = 0; jj < kNumChunks; ++jj) {
                     const int j = (jj == 0) ? 8 : jj - 1;  // rope chunk first
                     const uint32_t s = k_cnt % NK;
                     if (!ptx::mbar_wait_bounded(k_empty + s, ((k_cnt / NK) & 1) ^ 1, tmo)) return false;
                     if (leader) ptx::mbar_arrive_expect_tx(k_full + s, 2 * C::kKChunk);
                     if (!(stall_cta && unit == args.stall_unit))
-                        for (int i = 0; i < n_box; ++i)
+                        box.each([&](int i, int row, int page) {
                             ptx::tma_load_3d_pair(k_smem + s * C::kKChunk + i * box_bytes, &tm_k,
-                                                  ptx::mapa_shared(ptx::smem_u32(k_full + s), 0), j * kChunk, box[i].y,
-                                                  box[i].x);
+                                                  ptx::mapa_shared(ptx::smem_u32(k_full + s), 0), j * kChunk, row, page);
+                        });
                     ++unit;
                     ++k_cnt;
                 }
@@ -390,21 +388,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         // ============================================================ V producer
         if constexpr (CV::kPaged) {
             uint32_t v_cnt = 0;
-            BoxList<Walker> boxes(pa, walker, smem + C::OFF_LIST + 512, lane, 0, 7);
+            BoxList<Walker, 8> boxes(pa, walker, smem + C::OFF_LIST + 512, lane, 0, 7);
             const uint32_t box_bytes = 256u << pa.box_log2;  // two chunks
-            const bool ok = boxes.run(args.status, [&](auto count, int tile, bool) -> bool {
-                constexpr int n_box = decltype(count)::value;
-                int2 box[n_box];
-                boxes.template get<n_box>(tile, box);
+            const bool ok = boxes.run(args.status, [&](int tile, bool) -> bool {
+                const auto box = boxes.get(tile);
+#pragma unroll 1
                 for (int i = 0; i < 2; ++i) {
                     const uint32_t s = v_cnt % NV;
                     if (!ptx::mbar_wait_bounded(v_empty + s, ((v_cnt / NV) & 1) ^ 1, tmo)) return false;
                     if (leader) ptx::mbar_arrive_expect_tx(v_full + s, 2 * C::kVSlot);
                     const int col0 = 256 * i + 128 * static_cast<int>(rank);  // two adjacent chunks, one box
-                    for (int k = 0; k < n_box; ++k)
+                    box.each([&](int k, int row, int page) {
                         ptx::tma_load_4d_pair(v_smem + s * C::kVSlot + k * box_bytes, &tm_v,
-                                              ptx::mapa_shared(ptx::smem_u32(v_full + s), 0), 0, box[k].y,
-                                              col0 / kChunk, box[k].x);
+                                              ptx::mapa_shared(ptx::smem_u32(v_full + s), 0), 0, row, col0 / kChunk,
+                                              page);
+                    });
                     ++v_cnt;
                 }
                 return true;

@@ -444,10 +444,9 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
             int unit = 0, t = 0;
             Piece pc;
             bool open = false;  // tiles of pc are left
-            BoxList<Walker> boxes(pa, walker, smem + C::OFF_LIST, lane, 0, 7);
+            BoxList<Walker, 8> boxes(pa, walker, smem + C::OFF_LIST, lane, 0, 7);
             const uint32_t box_bytes = 128u << pa.box_log2;  // a box row is 128 bytes
-            const bool ok = boxes.run(args.status, [&](auto count, int tile, bool) -> bool {
-                constexpr int n_box = decltype(count)::value;
+            const bool ok = boxes.run(args.status, [&](int tile, bool) -> bool {
                 const bool may_stall = blockIdx.x == 0;
                 if (!open) {
                     walker.next(pc);
@@ -472,27 +471,27 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                     ++unit;
                     ++piece_cnt;
                 }
-                int2 box[n_box];
-                boxes.template get<n_box>(tile, box);
+                const auto box = boxes.get(tile);
                 if constexpr (!SH::kMha) {
                     const uint32_t s = rope_cnt % C::NR;
                     if (!ptx::mbar_wait_bounded(rope_empty + s, ((rope_cnt / C::NR) & 1) ^ 1, tmo)) return false;
                     ptx::mbar_arrive_expect_tx(rope_full + s, C::kChunkBytes);
                     if (!(may_stall && unit == args.stall_unit))
-                        for (int i = 0; i < n_box; ++i)
+                        box.each([&](int i, int row, int page) {
                             ptx::tma_load_3d(rope_smem + s * C::kChunkBytes + i * box_bytes, &tm_kv, rope_full + s,
-                                             8 * kChunk, box[i].y, box[i].x);
+                                             8 * kChunk, row, page);
+                        });
                     ++unit;
                     ++rope_cnt;
                 }
+#pragma unroll 1
                 for (int pp = 0; pp < (SH::kMha ? 2 : 4); ++pp) {
                     const uint32_t s = pair_cnt % C::NP;
                     if (!ptx::mbar_wait_bounded(pair_empty + s, ((pair_cnt / C::NP) & 1) ^ 1, tmo)) return false;
                     ptx::mbar_arrive_expect_tx(pair_full + s, C::kPairBytes);
                     if (!(may_stall && unit == args.stall_unit))
-                        for (int i = 0; i < n_box; ++i) {
+                        box.each([&](int i, int row, int page) {
                             uint8_t* dst = pair_smem + s * C::kPairBytes + i * box_bytes;
-                            const int row = box[i].y, page = box[i].x;
                             if constexpr (SH::kMha) {  // the tile's K rows, then its V rows (kv head g)
                                 const CUtensorMap* tm = (pp == 0) ? &tm_kv : &tm_v;
                                 ptx::tma_load_4d(dst, tm, pair_full + s, 0, g, row, page);
@@ -502,7 +501,7 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                                 ptx::tma_load_3d(dst + C::kChunkBytes, &tm_kv, pair_full + s, (2 * pp + 1) * kChunk,
                                                  row, page);
                             }
-                        }
+                        });
                     ++unit;
                     ++pair_cnt;
                 }

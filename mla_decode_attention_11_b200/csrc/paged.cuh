@@ -18,6 +18,7 @@
 // outside it, which is also flagged.
 #pragma once
 
+#include <cuda.h>
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -40,6 +41,7 @@ struct PagedArgs {
     int window, first;         // window 0: no window
     int heads_log2;            // query rows per token (latent caches: H, a power of two)
     int whole_slot;            // >= 0: a whole sequence also leaves a partial, in slot whole_slot + b; -1: none does
+    CUtensorMap prefetch;      // E4M3 pages: boxes of `box` rows x all columns, for prefetches into L2
 };
 
 // One sequence as read: its length, and its rows as the tiles number them.
@@ -128,12 +130,8 @@ __device__ __forceinline__ bool tile_unseen(const PagedArgs& a, const SeqView& v
 // TMA's operands to be one thread's.  Polling, arming and issuing with the whole warp instead (a box a
 // lane) cost 23 % at 128 heads and 22 % over grouped kv heads even where a tile
 // is one box or two.
-template <int N>
-struct BoxCount {
-    static constexpr int value = N;
-};
-
-template <class Walker>
+// kMost: the most boxes of a tile.
+template <class Walker, int kMost>
 struct BoxList {
     static constexpr int kEntries = 64;
     static constexpr int kBytes = kEntries * 8;
@@ -154,31 +152,40 @@ struct BoxList {
         pc.tile_hi = 0;  // no piece yet
     }
 
-    // the N boxes of a tile
-    template <int N>
-    __device__ __forceinline__ void get(int tile, int2 (&box)[N]) const {
-        const int2* from = list + (tile * N & (kEntries - 1));
+    // calls load(i, row, page) for each box i of a tile
+    struct Boxes {
+        int2 box[kMost];
+        int count;
+        template <class Load>
+        __device__ __forceinline__ void each(Load load) const {
+            // counts are powers of two: one test settles the usual one or two boxes
+            load(0, box[0].y, box[0].x);
 #pragma unroll
-        for (int i = 0; i < N; ++i) box[i] = from[i];
+            for (int n = 1; n < kMost; n *= 2) {
+                if (n >= count) return;
+#pragma unroll
+                for (int i = n; i < 2 * n; ++i) load(i, box[i].y, box[i].x);
+            }
+        }
+    };
+    __device__ __forceinline__ Boxes get(int tile) const {
+        Boxes b;
+        b.count = 1 << n_log2;
+        const int2* from = list + ((tile << n_log2) & (kEntries - 1));
+        b.box[0] = from[0];
+#pragma unroll
+        for (int n = 1; n < kMost; n *= 2)
+            if (n < b.count)
+#pragma unroll
+                for (int i = n; i < 2 * n; ++i) b.box[i] = from[i];
+        return b;
     }
 
-    // run_n with the number of boxes of a tile, which the issuing code unrolls over.
+    // All lanes call it; the elected one (always the same) calls
+    // issue(tile, more) for each tile in order until it returns false.  more: the
+    // next tile's boxes are known too.
     template <class Issue>
     __device__ __forceinline__ bool run(uint32_t* status, Issue issue) {
-        switch (n_log2) {
-            case 0: return run_n<1>(status, issue);
-            case 1: return run_n<2>(status, issue);
-            case 2: return run_n<4>(status, issue);
-            default: return run_n<8>(status, issue);
-        }
-    }
-
-private:
-    // All lanes call it; the elected one (always the same) calls
-    // issue(N, tile, more) for each tile in order until it returns false.  more:
-    // the next tile's boxes are known too.
-    template <int N, class Issue>
-    __device__ __forceinline__ bool run_n(uint32_t* status, Issue issue) {
         // one copy of each step, and few instructions before the first load: at the
         // start of a kernel every line of code is fetched from L2 or beyond
         int done = 0, known = 0;
@@ -188,7 +195,7 @@ private:
             // the last known tile waits for the next one to be known
             const int limit = tiles == 0 ? known : known - 1;
             if (ptx::elect_one())
-                for (int i = done; ok && i < limit; ++i) ok = issue(BoxCount<N>{}, i, i + 1 < known);
+                for (int i = done; ok && i < limit; ++i) ok = issue(i, i + 1 < known);
             done = limit > done ? limit : done;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || tiles == 0) return ok;

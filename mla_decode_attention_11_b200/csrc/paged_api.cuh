@@ -275,9 +275,11 @@ mla_status mla_decode_run_paged_fp8(const mla_plan* plan, const void* q, const v
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * kv_scale * 1.4426950408889634074);
     a.o_scale = kv_scale;
-    const mla::PagedArgs pa = paged_args(pl, seqlens, block_table, table_stride, num_pages, false);
+    mla::PagedArgs pa = paged_args(pl, seqlens, block_table, table_stride, num_pages, false);
     CUtensorMap tm_kv;
-    if (!encode_kv_fp8(enc, &tm_kv, kv_pages, pl.page_size, num_pages, pa.box)) return MLA_ERR_CUDA;
+    if (!encode_kv_fp8(enc, &tm_kv, kv_pages, pl.page_size, num_pages, pa.box) ||
+        !encode_kv_fp8_chunks(enc, &pa.prefetch, kv_pages, pl.page_size, num_pages, pa.box, mla::kNumChunks))
+        return MLA_ERR_CUDA;
     st = (G == 16) ? launch_fp8mma<16, mla::PagedKv>(pl, tm_kv, a, pa, stream)
                    : launch_fp8mma<32, mla::PagedKv>(pl, tm_kv, a, pa, stream);
     if (st != MLA_OK) {

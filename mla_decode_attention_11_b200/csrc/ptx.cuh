@@ -72,11 +72,15 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 // `timeout_ns` nanoseconds of %globaltimer.  Returns false on timeout; the
 // caller records the error and leaves its loop (no trap, no endless spin).
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t it = 0;; ++it) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 63u) == 0u && globaltimer_ns() - t0 > timeout_ns) return false;
+        if ((it & 63u) == 0u) {
+            const uint64_t t = globaltimer_ns();
+            if (it == 0) t0 = t;
+            if (t - t0 > timeout_ns) return false;
+        }
     }
 }
 
@@ -291,11 +295,15 @@ __device__ __forceinline__ bool mbar_try_wait_acq_cluster(uint64_t* bar, uint32_
 // Bounded wait with cluster-scope acquire (for barriers that the peer CTA's
 // threads arrive on after writing data this CTA's MMAs read).
 __device__ __forceinline__ bool mbar_wait_bounded_cluster(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
-    if (mbar_try_wait_acq_cluster(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t it = 0;; ++it) {
         if (mbar_try_wait_acq_cluster(bar, parity)) return true;
-        if ((it & 63u) == 0u && globaltimer_ns() - t0 > timeout_ns) return false;
+        if ((it & 63u) == 0u) {
+            const uint64_t t = globaltimer_ns();
+            if (it == 0) t0 = t;
+            if (t - t0 > timeout_ns) return false;
+        }
     }
 }
 

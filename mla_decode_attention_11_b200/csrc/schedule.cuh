@@ -54,7 +54,7 @@ __device__ __forceinline__ int num_tiles(int L) { return (L + kTileKV - 1) / kTi
 
 // schedule units of a sequence of L keys: its tiles (S = 0) or its S-tile chunks
 __device__ __forceinline__ long long num_units(int L, int S) {
-    const long long n = num_tiles(L);
+    const int n = num_tiles(L);
     return S > 0 ? (n + S - 1) / S : n;
 }
 
@@ -220,8 +220,8 @@ struct PieceWalkerOf {
     __device__ bool next_chunk(Piece& out) {
         while (b < B && acc + k < end) {
             const int L = lens(b);
-            const long long n = num_tiles(L);
-            const long long u = (n + S - 1) / S;
+            const int n = num_tiles(L);  // < 2^18, and so is S: 32-bit division
+            const int u = (n + S - 1) / S;
             if (acc + k < start) k = start - acc;
             if (k >= u) {
                 acc += u;
