@@ -236,6 +236,8 @@ def mla_decode_workspace_init(plan: mla_plan, workspace: torch.Tensor, stream=No
 
 
 def _check_tensor(t: torch.Tensor, name: str, dtype, shape) -> None:
+    if t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -555,28 +557,42 @@ def mla_decode_plan_prefix(B: int, Sq: int, H: int, L_max: int, prefix_max: int,
     return p
 
 
+# The current stream's handle without building a torch.cuda.Stream (3 us of the
+# 10 to 15 that one of the calls below takes on the host).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(device: int, stream) -> int:
+    return _raw_stream(device) if stream is None and _raw_stream is not None else _stream_handle(stream)
+
+
 def _check_table(t: torch.Tensor, name: str, rows: Optional[int]) -> None:
+    shape = t.shape
+    if (t.is_cuda and t.dtype == torch.int32 and len(shape) == (1 if rows is None else 2) and shape[-1] > 0 and
+            (rows is None or shape[0] == rows) and (shape[-1] == 1 or t.stride()[-1] == 1)):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.int32:
         raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-    if t.dim() != (1 if rows is None else 2) or (rows is not None and t.shape[0] != rows) or t.shape[-1] < 1:
+    if t.dim() != (1 if rows is None else 2) or (rows is not None and shape[0] != rows) or shape[-1] < 1:
         raise ValueError(f"{name} must have shape {'(width,)' if rows is None else f'({rows}, width)'}, "
-                         f"got {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the entries of a row must be contiguous")
+                         f"got {tuple(shape)}")
+    raise ValueError(f"{name}: the entries of a row must be contiguous")
 
 
-def _check_device(device, tensors) -> None:
+def _check_device(device: int, tensors) -> None:
+    """Every tensor is on `device`, and it is the current one."""
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors must be on {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, which is not the current device")
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"all tensors must be on cuda:{device}, got {t.device}")
+    if device != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{device}, which is not the current device")
 
 
 def _check_paged(plan, q, pages, seqlens, block_table, out, lse, sinks, workspace, d_key, d_value, page_row,
                  dtype=torch.bfloat16):
+    """Checks what the paged decodes share; the device's index."""
     B, Sq, H = plan.B, plan.Sq, plan.H
     _check_tensor(q, "q", torch.bfloat16, (B, Sq, H, d_key))
     for name, p in pages:
@@ -587,7 +603,9 @@ def _check_paged(plan, q, pages, seqlens, block_table, out, lse, sinks, workspac
     _check_tensor(lse, "lse", torch.float32, (B, Sq, H))
     if sinks is not None:
         _check_tensor(sinks, "sinks", torch.float32, (H,))
-    _check_device(q.device, (seqlens, block_table, out, lse, sinks, workspace, *(p for _, p in pages)))
+    device = q.get_device()
+    _check_device(device, (seqlens, block_table, out, lse, sinks, workspace, *[p for _, p in pages]))
+    return device
 
 
 def mla_decode_run_paged(plan: mla_plan, q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tensor,
@@ -596,14 +614,14 @@ def mla_decode_run_paged(plan: mla_plan, q: torch.Tensor, kv_pages: torch.Tensor
     """Enqueue one decode over a paged cache: kv_pages bf16 [pages, page_size,
     576], block_table int32 [B, width] (rows may be strided), seqlens the
     lengths with the query tokens' own keys."""
-    _check_paged(plan, q, (("kv_pages", kv_pages),), seqlens, block_table, out, lse, sinks, workspace, D_QK, D_V,
-                 (D_QK,))
+    device = _check_paged(plan, q, (("kv_pages", kv_pages),), seqlens, block_table, out, lse, sinks, workspace,
+                          D_QK, D_V, (D_QK,))
     rc = load_library().mla_decode_run_paged(ctypes.byref(plan), q.data_ptr(), kv_pages.data_ptr(), kv_pages.shape[0],
                                              block_table.data_ptr(), block_table.stride(0), block_table.shape[1],
                                              seqlens.data_ptr(), float(softmax_scale),
                                              sinks.data_ptr() if sinks is not None else None, out.data_ptr(),
                                              lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                             _stream_handle(stream))
+                                             _stream_on(device, stream))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_decode_run_paged")
 
@@ -615,14 +633,14 @@ def mla_decode_run_paged_fp8(plan: mla_plan, q: torch.Tensor, kv_pages: torch.Te
     """mla_decode_run_paged over pages of E4M3 codes (torch.uint8 or
     torch.float8_e4m3fn) that stand for code * kv_scale."""
     pages = _fp8_codes(kv_pages)
-    _check_paged(plan, q, (("kv_pages", pages),), seqlens, block_table, out, lse, sinks, workspace, D_QK, D_V,
-                 (D_QK,), torch.uint8)
+    device = _check_paged(plan, q, (("kv_pages", pages),), seqlens, block_table, out, lse, sinks, workspace,
+                          D_QK, D_V, (D_QK,), torch.uint8)
     rc = load_library().mla_decode_run_paged_fp8(ctypes.byref(plan), q.data_ptr(), pages.data_ptr(), pages.shape[0],
                                                  float(kv_scale), block_table.data_ptr(), block_table.stride(0),
                                                  block_table.shape[1], seqlens.data_ptr(), float(softmax_scale),
                                                  sinks.data_ptr() if sinks is not None else None, out.data_ptr(),
                                                  lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                                 _stream_handle(stream))
+                                                 _stream_on(device, stream))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_decode_run_paged_fp8")
 
@@ -634,14 +652,14 @@ def mha_decode_run_paged(plan: mla_plan, q: torch.Tensor, k_pages: torch.Tensor,
     """Enqueue one MHA decode over key and value pages bf16 [pages, page_size, Hkv, 128]."""
     if v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must have the same shape")
-    _check_paged(plan, q, (("k_pages", k_pages), ("v_pages", v_pages)), seqlens, block_table, out, lse, sinks,
-                 workspace, MHA_D, MHA_D, (plan.Hkv, MHA_D))
+    device = _check_paged(plan, q, (("k_pages", k_pages), ("v_pages", v_pages)), seqlens, block_table, out, lse,
+                          sinks, workspace, MHA_D, MHA_D, (plan.Hkv, MHA_D))
     rc = load_library().mha_decode_run_paged(ctypes.byref(plan), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                                              k_pages.shape[0], block_table.data_ptr(), block_table.stride(0),
                                              block_table.shape[1], seqlens.data_ptr(), float(softmax_scale),
                                              sinks.data_ptr() if sinks is not None else None, out.data_ptr(),
                                              lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                             _stream_handle(stream))
+                                             _stream_on(device, stream))
     if rc != MLA_OK:
         raise MlaError(rc, "mha_decode_run_paged")
 
@@ -653,18 +671,18 @@ def mla_decode_run_prefix(plan: mla_plan, q: torch.Tensor, kv_pages: torch.Tenso
     """Enqueue one decode of a batch with a shared prefix: prefix_table int32
     [width] the prefix's pages, prefix_len int32 [1] on the device, seqlens the
     sequences' own keys (the query tokens' among them), found in block_table."""
-    _check_paged(plan, q, (("kv_pages", kv_pages),), seqlens, block_table, out, lse, sinks, workspace, D_QK, D_V,
-                 (D_QK,))
+    device = _check_paged(plan, q, (("kv_pages", kv_pages),), seqlens, block_table, out, lse, sinks, workspace,
+                          D_QK, D_V, (D_QK,))
     _check_table(prefix_table, "prefix_table", None)
     _check_tensor(prefix_len, "prefix_len", torch.int32, (1,))
-    _check_device(q.device, (prefix_table, prefix_len))
+    _check_device(device, (prefix_table, prefix_len))
     rc = load_library().mla_decode_run_prefix(ctypes.byref(plan), q.data_ptr(), kv_pages.data_ptr(), kv_pages.shape[0],
                                               prefix_table.data_ptr(), prefix_table.shape[0], prefix_len.data_ptr(),
                                               block_table.data_ptr(), block_table.stride(0), block_table.shape[1],
                                               seqlens.data_ptr(), float(softmax_scale),
                                               sinks.data_ptr() if sinks is not None else None, out.data_ptr(),
                                               lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                              _stream_handle(stream))
+                                              _stream_on(device, stream))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_decode_run_prefix")
 
@@ -682,22 +700,23 @@ _APPEND = struct.Struct("=10iq10Q8qQfi")  # the fields of mla_append, in order
 
 def _check_rows(t: torch.Tensor, name: str, shape) -> None:
     """bf16 rows [T, (heads,) width]: any strides but the last."""
+    if t.is_cuda and t.dtype == torch.bfloat16 and t.shape == shape and t.stride()[-1] == 1:
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
+    raise ValueError(f"{name}: the last dimension must be contiguous")
 
 
 def _strides(t: Optional[torch.Tensor]) -> Tuple[int, int]:
     """(token, head) element strides; 0 where there is one token or head (or no head axis)."""
     if t is None:
         return 0, 0
-    return (t.stride(0) if t.shape[0] > 1 else 0,
-            t.stride(1) if t.dim() == 3 and t.shape[1] > 1 else 0)
+    shape, stride = t.shape, t.stride()
+    return (stride[0] if shape[0] > 1 else 0), (stride[1] if len(shape) == 3 and shape[1] > 1 else 0)
 
 
 def _append(name, k, v, cos_sin, k_pages, v_pages, block_table, seqlens, cu_tokens, q_in, q_out, q_out_offset,
@@ -710,25 +729,25 @@ def _append(name, k, v, cos_sin, k_pages, v_pages, block_table, seqlens, cu_toke
         raise ValueError(f"cos_sin must have shape (positions, rotated columns), got {tuple(cos_sin.shape)}")
     if cu_tokens is not None:
         _check_tensor(cu_tokens, "cu_tokens", torch.int32, (B + 1,))
-    H = 0
+    H, out_strides = 0, _strides(q_out)
     if q_in is not None:
         H = q_in.shape[1]
-        for i in range(2):
-            if q_out.shape[i] > 1 and q_out.stride(i) == 0:
-                raise ValueError("the rotated queries' rows must not share memory")
+        if (T > 1 and out_strides[0] == 0) or (H > 1 and out_strides[1] == 0):
+            raise ValueError("the rotated queries' rows must not share memory")
     elif q_out is not None:
         raise ValueError("rotated queries need both their input and their output")
-    _check_device(k.device, (v, cos_sin, k_pages, v_pages, block_table, seqlens, cu_tokens, q_in, q_out, workspace))
+    device = k.get_device()
+    _check_device(device, (v, cos_sin, k_pages, v_pages, block_table, seqlens, cu_tokens, q_in, q_out, workspace))
+    positions, rot = cos_sin.shape
+    pages, page_size = k_pages.shape[:2]
     args = _APPEND.pack(
-        B, T, H, Hkv, cos_sin.shape[1], 1 if interleaved else 0, cos_sin.shape[0], k_pages.shape[1],
-        k_pages.shape[0], block_table.shape[1], block_table.stride(0),
-        cu_tokens.data_ptr() if cu_tokens is not None else 0, seqlens.data_ptr(), block_table.data_ptr(),
-        cos_sin.data_ptr(), k.data_ptr(), v.data_ptr(), q_in.data_ptr() if H else 0,
+        B, T, H, Hkv, rot, 1 if interleaved else 0, positions, page_size, pages, block_table.shape[1],
+        block_table.stride()[0], cu_tokens.data_ptr() if cu_tokens is not None else 0, seqlens.data_ptr(),
+        block_table.data_ptr(), cos_sin.data_ptr(), k.data_ptr(), v.data_ptr(), q_in.data_ptr() if H else 0,
         q_out.data_ptr() + q_out_offset if H else 0, k_pages.data_ptr(),
-        v_pages.data_ptr() if v_pages is not None else 0, *_strides(k), *_strides(v), *_strides(q_in),
-        *_strides(q_out), workspace.data_ptr() if workspace is not None else 0, kv_scale, 0)
-    lib = load_library()
-    rc = getattr(lib, name)(args, _stream_handle(stream))
+        v_pages.data_ptr() if v_pages is not None else 0, *_strides(k), *_strides(v), *_strides(q_in), *out_strides,
+        workspace.data_ptr() if workspace is not None else 0, kv_scale, 0)
+    rc = getattr(load_library(), name)(args, _stream_on(device, stream))
     if rc != MLA_OK:
         raise MlaError(rc, name)
 
