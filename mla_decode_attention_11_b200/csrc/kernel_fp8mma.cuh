@@ -786,14 +786,13 @@ __global__ void __launch_bounds__(192, 1)
                     ptx::tmem_ld_16(lane_addr + blk * C::NO + c0, r1);
                     ptx::tmem_ld_16(lane_addr + blk * C::NO + G + c0, r2);
                     ptx::tmem_wait_ld();
+                    auto store = [&](auto* dst) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float o = (__uint_as_float(r1[j]) + __uint_as_float(r2[j])) * fin[c0 + j];
-                        if (pc.slot < 0)
-                            args.out[at + j * kDv] = __float2bfloat16_rn(o);
-                        else
-                            args.part_o[at + j * kDv] = o;
-                    }
+                        for (int j = 0; j < 16; ++j)
+                            put(dst + at + j * kDv, (__uint_as_float(r1[j]) + __uint_as_float(r2[j])) * fin[c0 + j]);
+                    };
+                    if (pc.slot < 0) store(args.out);
+                    else store(args.part_o);
                 }
             }
             ptx::tc_fence_before();

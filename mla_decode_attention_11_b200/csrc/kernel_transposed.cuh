@@ -250,6 +250,9 @@ __device__ __forceinline__ void widen_chunk_row(const uint8_t* f8, uint8_t* dst,
     }
 }
 
+__device__ __forceinline__ void put(__nv_bfloat16* dst, float v) { *dst = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(float* dst, float v) { *dst = v; }
+
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -1023,26 +1026,26 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                 for (int blk = 0; blk < SH::kDvBlocks; ++blk) {
                     const int dv = blk * 128 + row_in_tile;
                     const size_t row0 = static_cast<size_t>(slot < 0 ? pc.b : slot) * args.R + group_row<SH>(args, G, g, c0);
-                    int rem = SH::kMha ? c0 % (args.H / args.Hkv) : 0;  // MHA: column within its token's
+                    const int gq = SH::kMha ? args.H / args.Hkv : 1;
+                    int rem = SH::kMha ? c0 % gq : 0;  // MHA: column within its token's
                     size_t at = row0 * SH::kDv + dv;
                     uint32_t r[16];
                     ptx::tmem_ld_16(lane_addr + blk * G + c0, r);
                     ptx::tmem_wait_ld();
+                    auto store = [&](auto* dst) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (!SH::kMha || c0 + j < n_cols) {
-                            const float o = __uint_as_float(r[j]) * fin[c0 + j];
-                            if (slot < 0)
-                                args.out[at] = __float2bfloat16_rn(o);
-                            else
-                                args.part_o[at] = o;
+                        for (int j = 0; j < 16; ++j) {
+                            if (!SH::kMha || c0 + j < n_cols)
+                                put(dst + at, __uint_as_float(r[j]) * fin[c0 + j]);
+                            at += SH::kDv;
+                            if (SH::kMha && ++rem == gq) {  // the next token's heads
+                                rem = 0;
+                                at += static_cast<size_t>(args.H - gq) * SH::kDv;
+                            }
                         }
-                        at += SH::kDv;
-                        if (SH::kMha && ++rem == args.H / args.Hkv) {  // the next token's heads
-                            rem = 0;
-                            at += static_cast<size_t>(args.H - args.H / args.Hkv) * SH::kDv;
-                        }
-                    }
+                    };
+                    if (slot < 0) store(args.out);
+                    else store(args.part_o);
                 }
             }
             ptx::tc_fence_before();
