@@ -584,11 +584,13 @@ __global__ void __launch_bounds__(192, 1)
             if (!ok) break;
 
             SeqView view{};
-            int all_lo = 0, all_hi = 0;  // paged: the rows that every query row of the group sees
+            int all_f = 0, all_lo = 0, all_hi = 0;  // paged: every query row of the group sees rows [0, f) and [lo, hi)
             if constexpr (CV::kPaged) {
                 view = view_of(pa, paged_len(pa, pc.b));
                 all_lo = token_rows(pa, view, (g * G + G - 1) >> pa.heads_log2).b0;
-                all_hi = token_rows(pa, view, (g * G) >> pa.heads_log2).b1;
+                const RowRange least = token_rows(pa, view, (g * G) >> pa.heads_log2);
+                all_f = least.f;
+                all_hi = least.b1;
             }
             float m_ref[G];
             float l_part[G];
@@ -606,7 +608,7 @@ __global__ void __launch_bounds__(192, 1)
 
                 uint32_t hidden = 0;
                 if constexpr (CV::kPaged) {
-                    if (row0 < all_lo || row0 + kTileKV > all_hi)
+                    if ((row0 < all_lo || row0 + kTileKV > all_hi) && row0 + kTileKV > all_f)
                         hidden = hidden_columns(pa, view, G, (g * G) >> pa.heads_log2,
                                                 (g * G) & ((1 << pa.heads_log2) - 1), 1 << pa.heads_log2, kv_row);
                 }

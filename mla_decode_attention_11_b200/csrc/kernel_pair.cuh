@@ -200,6 +200,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             int n = args.B;
             if constexpr (CV::kPaged) n = pa.len_stride ? n : 1;
             for (int b = lane; b < n; b += 32) clamp_len(args.seqlens[b], args.L_max, args.status);
+            if constexpr (CV::kPaged)
+                if (pa.prefix_table) clamp_len(*pa.prefix_len, pa.prefix_max, args.status);
         }
     }
     if (warp == 4 && lane == 0) {

@@ -402,8 +402,11 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
             *split_slot = S_eff;
         }
         // flag out-of-range lengths once (partition 0, group 0 only)
-        if (blockIdx.x == 0)
+        if (blockIdx.x == 0) {
             for (int b = lane; b < args.B; b += 32) clamp_len(args.seqlens[b], args.L_max, args.status);
+            if constexpr (CV::kPaged)
+                if (pa.prefix_table) clamp_len(*pa.prefix_len, pa.prefix_max, args.status);
+        }
     }
     if (warp == 4 && lane == 0) {
         ptx::prefetch_tmap(&tm_q);
@@ -829,12 +832,14 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
         Piece pc;
         while (ok && walker.next(pc)) {
             SeqView view{};
-            int all_lo = 0, all_hi = 0;  // paged: the rows that every query row of the group sees
+            int all_f = 0, all_lo = 0, all_hi = 0;  // paged: every query row of the group sees rows [0, f) and [lo, hi)
             if constexpr (CV::kPaged) {
                 view = view_of(pa, paged_len(pa, pc.b));
                 const int last = SH::kMha ? pa.Sq - 1 : (g * G + G - 1) >> pa.heads_log2;
                 all_lo = token_rows(pa, view, last).b0;
-                all_hi = token_rows(pa, view, SH::kMha ? 0 : (g * G) >> pa.heads_log2).b1;
+                const RowRange least = token_rows(pa, view, SH::kMha ? 0 : (g * G) >> pa.heads_log2);
+                all_f = least.f;
+                all_hi = least.b1;
             }
             float m_ref[G];
             float l_part[G];
@@ -853,7 +858,7 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
                 uint32_t hidden = 0;
                 if constexpr (CV::kPaged) {
                     const int r0 = SH::kMha ? 0 : g * G;
-                    if (row0 < all_lo || row0 + kTileKV > all_hi)
+                    if ((row0 < all_lo || row0 + kTileKV > all_hi) && row0 + kTileKV > all_f)
                         hidden = hidden_columns(pa, view, G, SH::kMha ? 0 : r0 >> pa.heads_log2,
                                                 SH::kMha ? 0 : r0 & ((1 << pa.heads_log2) - 1),
                                                 SH::kMha ? args.H / args.Hkv : 1 << pa.heads_log2, kv_row);

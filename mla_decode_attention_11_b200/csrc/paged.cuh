@@ -10,7 +10,9 @@
 // the sequence as the schedule and the tiles see it.  Its rows are numbered by
 //     i < split:  position i            (boxes of the first tokens)
 //     i >= split: position i + jump     (boxes from the one that holds lo)
-// with jump = 0 where nothing is left out.  Rows that no token sees -- past L,
+// with jump = 0 where nothing is left out.  Behind a shared prefix of P keys the
+// rows below split = P rounded up to a box are the prefix's, found in its own
+// table, and the sequence's own keys follow with jump = -split.  Rows that no token sees -- past L,
 // and around the ends of the two ranges in their boxes -- are masked in S and
 // zeroed in shared memory before P V, so whatever they hold (a page's old
 // contents, NaN) reaches no result.  Boxes past the end are loaded with a page
@@ -40,16 +42,20 @@ struct PagedArgs {
     int Sq;                    // query tokens (positions count back from L)
     int window, first;         // window 0: no window
     int heads_log2;            // query rows per token (latent caches: H, a power of two)
+    // a shared prefix in front of every sequence's own keys, or null
+    const int32_t* prefix_table;
+    const int32_t* prefix_len;  // one length
+    int prefix_max;
     int whole_slot;            // >= 0: a whole sequence also leaves a partial, in slot whole_slot + b; -1: none does
     CUtensorMap prefetch;      // E4M3 pages: boxes of `box` rows x all columns, for prefetches into L2
 };
 
 // One sequence as read: its length, and its rows as the tiles number them.
 struct SeqView {
-    int L;      // keys
+    int L;      // keys (own keys behind a prefix)
     int rows;   // rows read (tiles cover these)
     int split, jump;
-    int lo;     // row of the first key seen through the window (0: no window)
+    int f, lo;  // rows [f, lo) are seen by no token
 };
 
 __device__ __forceinline__ SeqView view_of(const PagedArgs& a, int L) {
@@ -57,7 +63,14 @@ __device__ __forceinline__ SeqView view_of(const PagedArgs& a, int L) {
     v.L = L;
     v.rows = L;
     v.split = v.jump = v.lo = 0;
-    if (a.window > 0) {
+    v.f = a.first;
+    if (a.prefix_table) {
+        const int P = clamp_len(__ldg(a.prefix_len), a.prefix_max, nullptr);
+        v.f = P;
+        v.split = v.lo = ((P + a.box - 1) >> a.box_log2) << a.box_log2;
+        v.jump = -v.split;
+        v.rows = L > 0 ? v.split + L : P;
+    } else if (a.window > 0) {
         const int lo = L - a.Sq + 1 - a.window;
         if (lo > 0) {
             const int split = ((a.first + a.box - 1) >> a.box_log2) << a.box_log2;
@@ -88,7 +101,7 @@ struct RowRange {
     int f, b0, b1;
     __device__ __forceinline__ bool sees(int i) const { return i < f || (i >= b0 && i < b1); }
     // every row of [i, i + n) is seen
-    __device__ __forceinline__ bool all(int i, int n) const { return i >= b0 && i + n <= b1; }
+    __device__ __forceinline__ bool all(int i, int n) const { return (i >= b0 && i + n <= b1) || i + n <= f; }
 };
 
 __device__ __forceinline__ RowRange token_rows(const PagedArgs& a, const SeqView& v, int t) {
@@ -97,7 +110,10 @@ __device__ __forceinline__ RowRange token_rows(const PagedArgs& a, const SeqView
     r.f = 0;
     r.b0 = 0;
     r.b1 = p + 1 - v.jump;
-    if (a.window > 0) {
+    if (a.prefix_table) {
+        r.f = v.f;
+        r.b0 = v.split;
+    } else if (a.window > 0) {
         r.f = a.first < p + 1 ? a.first : p + 1;
         const int lo = p + 1 - a.window;
         if (lo > 0) r.b0 = lo - v.jump > 0 ? lo - v.jump : 0;
@@ -113,12 +129,12 @@ __device__ __forceinline__ uint64_t bits_between(int lo, int hi) {
 
 // Row i of a sequence is seen by none of its tokens.
 __device__ __forceinline__ bool unseen(const PagedArgs& a, const SeqView& v, int i) {
-    return i >= v.rows || (i < v.lo && i >= a.first);
+    return i >= v.rows || (i < v.lo && i >= v.f);
 }
 // Some row of tile t is seen by none: the tile's values are cleared there.
 __device__ __forceinline__ bool tile_unseen(const PagedArgs& a, const SeqView& v, int t) {
     const int i = t * kTileKV;
-    return i + kTileKV > v.rows || (i < v.lo && i + kTileKV > a.first);
+    return i + kTileKV > v.rows || (i < v.lo && i + kTileKV > v.f);
 }
 
 // The boxes of a partition's tiles, found by a producer warp for the one of its
@@ -220,7 +236,8 @@ struct BoxList {
                 if (i < v.rows) {
                     const int pos = i < v.split ? i : i + v.jump;
                     const int e = static_cast<int>(static_cast<uint64_t>(pos) * a.page_mul >> a.page_shift);
-                    page = __ldg(a.table + pc.b * a.table_stride + e);
+                    const bool shared = a.prefix_table && i < v.split;
+                    page = __ldg((shared ? a.prefix_table : a.table + pc.b * a.table_stride) + e);
                     row = pos - e * a.page_size;
                     some = true;
                 }

@@ -47,6 +47,19 @@ PrefixLayout prefix_layout(const mla_plan& pl) {
     return l;
 }
 
+// Whether every sequence reads the prefix in front of its own keys, in one
+// launch, or the prefix has a launch of its own for 128 rows of any sequences at
+// a time.  With 128 rows a sequence both do the same products, and one launch
+// balances them together and leaves no partial of a sequence that is not cut.
+// With fewer, a sequence's own pass over the prefix takes NG / 148 of its tiles'
+// time each; up to 4 tiles (about 12 us) a CTA that is less than the second
+// launch and the partials cost (about 20 us).
+bool prefix_in_front(const mla_plan& pl) {
+    if (pl.kernel == MLA_KERNEL_PAIR) return true;
+    const int64_t tiles = (static_cast<int64_t>(pl.prefix_max) + mla::kTileKV - 1) / mla::kTileKV;
+    return tiles * pl.B * pl.num_groups <= 4 * static_cast<int64_t>(pl.num_sms);
+}
+
 // Latent pages [num_pages, page_size, 576]: boxes of `rows` rows x 64 columns x
 // `chunks` adjacent 64-column chunks, chunk after chunk in shared memory
 // (chunks = 1: a 3-D map {576, page_size, num_pages}).
@@ -182,6 +195,42 @@ dim3 combine_grid(const mla_plan& pl) {
                 static_cast<unsigned>(mla::combine_grid_y(pl.B, pl.Sq * pl.H, pl.num_sms)));
 }
 
+struct Prefix {
+    const int32_t *table, *len;
+};
+
+// One decode over latent pages whose plan and arguments have been checked, the
+// workspace and the device excepted.
+mla_status run_mla_paged(const mla_plan& pl, const void* q, const void* kv_pages, int32_t num_pages,
+                         const Prefix* prefix, const int32_t* block_table, int64_t table_stride,
+                         const int32_t* seqlens, float softmax_scale, const float* sinks, void* out, float* lse,
+                         void* workspace, size_t workspace_bytes, void* stream_) {
+    const int R = pl.Sq * pl.H;
+    const Layout lay = workspace_layout(num_slots(pl), R);
+    if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
+    mla_status st = check_run_device(pl);
+    if (st != MLA_OK) return st;
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return MLA_ERR_CUDA;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    mla::MainArgs a;
+    main_args(a, pl, seqlens, softmax_scale, sinks, out, lse, workspace, lay.part_lse_off, lay.part_o_off);
+    mla::PagedArgs pa = paged_args(pl, seqlens, block_table, table_stride, num_pages, pl.kernel == MLA_KERNEL_PAIR);
+    if (prefix) {
+        pa.prefix_table = prefix->table;
+        pa.prefix_len = prefix->len;
+        pa.prefix_max = pl.prefix_max;
+    }
+    st = launch_mla_paged(enc, pl, q, static_cast<uint64_t>(pl.B) * R, kv_pages, a, pa,
+                          static_cast<uint64_t>(num_slots(pl)) * R, stream);
+    if (st != MLA_OK) {
+        cudaGetLastError();
+        return st;
+    }
+    return launch_dependent(mla::mla_decode_combine_kernel<mla::kDv, mla::PagedKv>, combine_grid(pl),
+                            mla::kCombineThreads, stream, combine_args(a), pa);
+}
+
 }  // namespace
 
 extern "C" {
@@ -205,32 +254,13 @@ mla_status mla_decode_plan_paged(int32_t B, int32_t Sq, int32_t H, int32_t L_max
 mla_status mla_decode_run_paged(const mla_plan* plan, const void* q, const void* kv_pages, int32_t num_pages,
                                 const int32_t* block_table, int64_t table_stride, int32_t table_width,
                                 const int32_t* seqlens, float softmax_scale, const float* sinks, void* out, float* lse,
-                                void* workspace, size_t workspace_bytes, void* stream_) {
-    mla_status st = check_paged(plan, q, kv_pages, kv_pages, num_pages, block_table, table_stride, table_width, seqlens,
-                                softmax_scale, sinks, out, lse);
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    const mla_status st = check_paged(plan, q, kv_pages, kv_pages, num_pages, block_table, table_stride, table_width,
+                                      seqlens, softmax_scale, sinks, out, lse);
     if (st != MLA_OK) return st;
-    const mla_plan& pl = *plan;
-    if (!mla_groups_ok(pl) || pl.prefix_max != 0) return MLA_ERR_INVALID_ARG;
-    const int R = pl.Sq * pl.H;
-    const Layout lay = workspace_layout(num_slots(pl), R);
-    if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
-    st = check_run_device(pl);
-    if (st != MLA_OK) return st;
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return MLA_ERR_CUDA;
-    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    mla::MainArgs a;
-    main_args(a, pl, seqlens, softmax_scale, sinks, out, lse, workspace, lay.part_lse_off, lay.part_o_off);
-    const mla::PagedArgs pa =
-        paged_args(pl, seqlens, block_table, table_stride, num_pages, pl.kernel == MLA_KERNEL_PAIR);
-    st = launch_mla_paged(enc, pl, q, static_cast<uint64_t>(pl.B) * R, kv_pages, a, pa,
-                          static_cast<uint64_t>(num_slots(pl)) * R, stream);
-    if (st != MLA_OK) {
-        cudaGetLastError();
-        return st;
-    }
-    return launch_dependent(mla::mla_decode_combine_kernel<mla::kDv, mla::PagedKv>, combine_grid(pl),
-                            mla::kCombineThreads, stream, combine_args(a), pa);
+    if (!mla_groups_ok(*plan) || plan->prefix_max != 0) return MLA_ERR_INVALID_ARG;
+    return run_mla_paged(*plan, q, kv_pages, num_pages, nullptr, block_table, table_stride, seqlens, softmax_scale,
+                         sinks, out, lse, workspace, workspace_bytes, stream);
 }
 
 mla_status mla_decode_plan_paged_fp8(int32_t B, int32_t Sq, int32_t H, int32_t L_max, int32_t page_size,
@@ -360,11 +390,13 @@ mla_status mla_decode_plan_prefix(int32_t B, int32_t Sq, int32_t H, int32_t L_ma
     if (st != MLA_OK) return st;
     p.page_size = page_size;
     p.prefix_max = prefix_max;
-    p.prefix_groups = static_cast<int32_t>((static_cast<int64_t>(B) * Sq * H + 127) / 128);
-    int P = num_partitions_override > 0 ? num_partitions_override : p.num_sms / 2;  // one CTA pair each
-    if (P < 1) P = 1;
-    p.prefix_partitions = P > 4096 ? 4096 : P;
-    p.workspace_bytes = prefix_layout(p).total;
+    if (!prefix_in_front(p)) {
+        p.prefix_groups = static_cast<int32_t>((static_cast<int64_t>(B) * Sq * H + 127) / 128);
+        int P = num_partitions_override > 0 ? num_partitions_override : p.num_sms / 2;  // one CTA pair each
+        if (P < 1) P = 1;
+        p.prefix_partitions = P > 4096 ? 4096 : P;
+        p.workspace_bytes = prefix_layout(p).total;
+    }
     *plan = p;
     if (workspace_bytes) *workspace_bytes = p.workspace_bytes;
     return MLA_OK;
@@ -381,11 +413,18 @@ mla_status mla_decode_run_prefix(const mla_plan* plan, const void* q, const void
     const mla_plan& pl = *plan;
     const int R = pl.Sq * pl.H;
     if (!prefix_table || !prefix_len || !mla_groups_ok(pl) || pl.window != 0 || pl.prefix_max < 1 ||
-        pl.prefix_max > (1 << 24) || pl.prefix_partitions < 1 || pl.prefix_partitions > 4096 ||
-        pl.prefix_groups != (static_cast<int64_t>(pl.B) * R + 127) / 128 || prefix_width < 1 ||
+        pl.prefix_max > (1 << 24) || prefix_width < 1 ||
         static_cast<int64_t>(prefix_width) * pl.page_size < pl.prefix_max)
         return MLA_ERR_INVALID_ARG;
     if (!aligned(prefix_table, 4) || !aligned(prefix_len, 4)) return MLA_ERR_ALIGNMENT;
+    if (pl.prefix_partitions == 0) {
+        const Prefix prefix = {prefix_table, prefix_len};
+        return run_mla_paged(pl, q, kv_pages, num_pages, &prefix, block_table, table_stride, seqlens, softmax_scale,
+                             sinks, out, lse, workspace, workspace_bytes, stream_);
+    }
+    if (pl.prefix_partitions < 1 || pl.prefix_partitions > 4096 ||
+        pl.prefix_groups != (static_cast<int64_t>(pl.B) * R + 127) / 128)
+        return MLA_ERR_INVALID_ARG;
     const PrefixLayout lay = prefix_layout(pl);
     if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
     st = check_run_device(pl);

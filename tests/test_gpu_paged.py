@@ -346,33 +346,41 @@ def make_prefix(lengths, Sq, H, P, page, sinks, seed, parts=0, prefix_max=None, 
     return run, ref, blank(B, Sq, H, 512), (plan, ws, pages, sl, pl)
 
 
+# a prefix planned as long as this has a launch of its own where a sequence has fewer than 128 query rows
+LONG = 1 << 18
+
+
 @pytest.mark.parametrize("parts", [0, 1, 7])
 @pytest.mark.parametrize("P", [0, 1, 100, 128, 500, 2049])
-@pytest.mark.parametrize("Sq,H", [(1, 16), (3, 16), (1, 64), (1, 128), (2, 128)])
-def test_prefix(cuda_device, Sq, H, P, parts):
+@pytest.mark.parametrize("Sq,H,most", [(1, 16, 0), (1, 16, LONG), (3, 16, 0), (3, 16, LONG), (1, 64, LONG), (2, 32, 0),
+                                       (1, 128, 0), (2, 128, 0)])
+def test_prefix(cuda_device, Sq, H, most, P, parts):
     lengths = [0, 1, 2, 17, 128, 129, 400]
     run, ref, (out, lse), (plan, ws, *_) = make_prefix(lengths, Sq, H, P, 16 if P < 200 else 64, H == 16, seed=P + H,
-                                                       parts=parts)
+                                                       parts=parts, prefix_max=most)
+    assert (plan.prefix_partitions > 0) == (most == LONG)
     run(out, lse)
     M.mla_decode_check(plan, ws)
     close(out, lse, ref, f"{Sq} {H} {P} {parts}")
 
 
+@pytest.mark.parametrize("most", [0, LONG])
 @pytest.mark.parametrize("B,Sq,H", [(1, 1, 16), (9, 1, 16), (300, 1, 16), (64, 1, 128), (33, 2, 32)])
-def test_prefix_batches(cuda_device, B, Sq, H):
+def test_prefix_batches(cuda_device, B, Sq, H, most):
     """Row groups of 128 that are not full, and more groups than partitions."""
     g = torch.Generator().manual_seed(B)
     lengths = torch.randint(0, 300, (B,), generator=g).tolist()
-    run, ref, (out, lse), (plan, ws, *_) = make_prefix(lengths, Sq, H, 900, 64, True, seed=B)
+    run, ref, (out, lse), (plan, ws, *_) = make_prefix(lengths, Sq, H, 900, 64, True, seed=B, prefix_max=most)
     run(out, lse)
     M.mla_decode_check(plan, ws)
     close(out, lse, ref)
 
 
-def test_prefix_shorter_than_planned_and_in_a_graph(cuda_device):
+@pytest.mark.parametrize("most", [5000, LONG])
+def test_prefix_shorter_than_planned_and_in_a_graph(cuda_device, most):
     """The prefix's length is read on the device: a captured call follows it."""
     run, ref, (out, lse), (plan, ws, pages, sl, pl) = make_prefix([30, 0, 200], 1, 64, 700, 32, False, seed=5,
-                                                                  prefix_max=5000, L_max=900)
+                                                                  prefix_max=most, L_max=900)
     run(out, lse)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
@@ -386,7 +394,7 @@ def test_prefix_shorter_than_planned_and_in_a_graph(cuda_device):
     graph.replay()
     M.mla_decode_check(plan, ws)
     assert torch.count_nonzero(out[1]) == 0 and (lse[1] == -math.inf).all()
-    pl.fill_(5001)
+    pl.fill_(most + 1)
     graph.replay()
     with pytest.raises(M.MlaError) as e:
         M.mla_decode_check(plan, ws)

@@ -26,10 +26,16 @@ def test_plans():
     assert M.mla_decode_plan_paged(4, 1, 16, 5000, 16, device=-1).kernel == M.MLA_KERNEL_TRANSPOSED
     assert M.mla_decode_plan_paged_fp8(4, 1, 128, 5000, 16, device=-1).kernel == M.MLA_KERNEL_FP8_MMA
     assert M.mha_decode_plan_paged(4, 1, 32, 8, 5000, 16, device=-1).kernel == M.MLA_KERNEL_MHA
-    p = M.mla_decode_plan_prefix(5, 2, 16, 100, 9000, 48, device=-1)
-    assert p.prefix_max == 9000 and p.prefix_groups == 2 and p.page_size == 48  # 160 rows: two groups of 128
+    # few heads and much to read: a launch of its own for the prefix, 160 rows in two groups of 128
+    p = M.mla_decode_plan_prefix(5, 2, 16, 100, 90000, 48, device=-1)
+    assert (p.prefix_max, p.prefix_groups, p.prefix_partitions, p.page_size) == (90000, 2, 74, 48)
     # one fp32 partial a query row for the prefix and one for its own keys
     assert p.workspace_bytes >= (p.prefix_groups * 128 + 160) * 513 * 4
+    # else the prefix is read in front of every sequence's keys, in one launch
+    for args in ((5, 2, 16, 100, 9000, 48), (64, 1, 128, 1000, 1 << 20, 64)):
+        p = M.mla_decode_plan_prefix(*args, device=-1)
+        assert p.prefix_groups == p.prefix_partitions == 0
+        assert p.workspace_bytes == M.mla_decode_plan(*args[:4], device=-1).workspace_bytes
 
 
 @pytest.mark.parametrize("page,window,first,code", [
