@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
     }
     // the prefix: every group has the same tiles
     const long long n_pre = num_tiles(PagedLens{&pre}(0));
-    const bool pre_one = pick_schedule(n_pre * args.groups, n_pre, args.groups, args.P_pre) > 0;
+    const bool pre_one = pick_schedule(n_pre * args.groups, n_pre, args.groups, args.P_pre, pre.cut_tiles) > 0;
     const long long T_pre = n_pre > 0 ? (n_pre * args.groups + args.P_pre - 1) / args.P_pre : 1;
 
     const int rows_per = (args.R + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);

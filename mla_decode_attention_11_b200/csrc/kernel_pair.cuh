@@ -874,6 +874,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         __syncwarp();
     }
 
+    // a launch that started before the one ahead of it was done ends after it
+    // (the merge that follows waits for this one only)
+    if constexpr (CV::kPaged) ptx::wait_prior_grid();
     // ---------------------------------------------------------------- teardown
     ptx::tc_fence_before();
     __syncthreads();

@@ -1123,6 +1123,9 @@ __global__ void __launch_bounds__(TransposedCfg<G, SH>::kThreads, 1)
         }
     }
 
+    // a launch that started before the one ahead of it was done ends after it
+    // (the merge that follows waits for this one only)
+    if constexpr (CV::kPaged) ptx::wait_prior_grid();
     // ---------------------------------------------------------------- teardown
     ptx::tc_fence_before();
     __syncthreads();

@@ -74,15 +74,39 @@ Layout workspace_layout(long long slots, int R, int dv = mla::kDv) {
     return l;
 }
 
+// A programmatic dependent of the kernel before it on the stream: its CTAs may
+// start (the combine scans the lengths) while that kernel finishes, and wait
+// in the kernel for that grid's results.
+template <class... Args, class... Given>
+mla_status launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t stream, int smem_bytes,
+                            const Given&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return MLA_ERR_CUDA;
+    }
+    return MLA_OK;
+}
+
 template <int G, class SH = mla::MlaShape, class CV = mla::ContigKv>
 mla_status launch_transposed(const mla_plan& plan, const CUtensorMap& tm_q, const CUtensorMap& tm_kv,
                              const CUtensorMap& tm_v, const mla::MainArgs& args, const typename CV::Args& pa,
-                             cudaStream_t stream) {
+                             cudaStream_t stream, bool overlap = false) {
     using C = mla::TransposedCfg<G, SH>;
     auto kern = mla::mla_decode_transposed_kernel<G, SH, CV>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
         return MLA_ERR_CUDA;
     const dim3 grid(static_cast<unsigned>(plan.num_partitions * plan.num_groups));
+    if (overlap) return launch_dependent(kern, grid, C::kThreads, stream, C::kSmemBytes, tm_q, tm_kv, tm_v, args, pa);
     kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(tm_q, tm_kv, tm_v, args, pa);
     return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
@@ -167,32 +191,9 @@ bool encode_rows_store(EncodeTiledFn enc, CUtensorMap* m, const void* base, uint
                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A programmatic dependent of the kernel before it on the stream: its CTAs may
-// start (the combine scans the lengths) while that kernel finishes, and wait
-// in the kernel for that grid's results.
-template <class... Args, class... Given>
-mla_status launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t stream,
-                            const Given&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = 0;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
-        cudaGetLastError();
-        return MLA_ERR_CUDA;
-    }
-    return MLA_OK;
-}
-
 template <int DV>
 mla_status launch_combine(dim3 grid, const mla::CombineArgs& c, cudaStream_t stream) {
-    return launch_dependent(mla::mla_decode_combine_kernel<DV>, grid, mla::kCombineThreads, stream, c,
+    return launch_dependent(mla::mla_decode_combine_kernel<DV>, grid, mla::kCombineThreads, stream, 0, c,
                             mla::ContigKv::Args{});
 }
 

@@ -39,6 +39,7 @@ struct PagedArgs {
     uint32_t page_mul;         // position / page_size = position * page_mul >> page_shift, for positions below 2^25
     int page_shift;
     int box, box_log2;         // rows per TMA box
+    int cut_tiles;             // the schedule's cost of a cut (schedule.cuh)
     int Sq;                    // query tokens (positions count back from L)
     int window, first;         // window 0: no window
     int heads_log2;            // query rows per token (latent caches: H, a power of two)
@@ -94,6 +95,7 @@ __device__ __forceinline__ int paged_len(const PagedArgs& a, int b) {
 struct PagedLens {
     const PagedArgs* a;  // the kernel's own parameter
     __device__ __forceinline__ int operator()(int b) const { return view_of(*a, paged_len(*a, b)).rows; }
+    __device__ __forceinline__ int cut() const { return a->cut_tiles; }
 };
 
 // Rows seen by one query token: [0, f) and [b0, b1).

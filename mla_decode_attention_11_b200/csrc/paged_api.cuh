@@ -32,6 +32,11 @@ struct PrefixLayout {
     size_t pre_lse, pre_o, own_lse, own_o, total;
 };
 
+// Where whole sequences leave a partial too, a cut costs less than kCutTiles:
+// 132 sequences of up to 16 tiles, 32 rows each, after a prefix of 16384 keys take
+// 218 us uncut, 206 cut into equal shares.
+constexpr int kPartialCutTiles = 2;
+
 // shared prefix: slots of the prefix's pieces (two per partition, one per
 // 128-row group) and of the sequences' own (two per partition, one per sequence)
 PrefixLayout prefix_layout(const mla_plan& pl) {
@@ -94,6 +99,7 @@ mla::PagedArgs paged_args(const mla_plan& pl, const int32_t* seqlens, const int3
     a.first = pl.first_tokens < pl.L_max ? pl.first_tokens : pl.L_max;
     while ((1 << a.heads_log2) < pl.H) ++a.heads_log2;
     a.whole_slot = -1;
+    a.cut_tiles = mla::kCutTiles;
     return a;
 }
 
@@ -153,7 +159,8 @@ bool mla_groups_ok(const mla_plan& pl) {
 
 // The main kernel of an MLA plan over pages.
 mla_status launch_mla_paged(EncodeTiledFn enc, const mla_plan& pl, const void* q, uint64_t q_rows, const void* kv,
-                            const mla::MainArgs& a, const mla::PagedArgs& pa, uint64_t part_rows, cudaStream_t stream) {
+                            const mla::MainArgs& a, const mla::PagedArgs& pa, uint64_t part_rows, cudaStream_t stream,
+                             bool overlap = false) {
     CUtensorMap tm_q, tm_k, tm_v, tm_pf, tm_out, tm_part;
     if (pl.kernel == MLA_KERNEL_PAIR) {
         if (!encode_q_chunks(enc, &tm_q, q, q_rows) ||
@@ -169,8 +176,8 @@ mla_status launch_mla_paged(EncodeTiledFn enc, const mla_plan& pl, const void* q
         !encode_pages(enc, &tm_k, kv, pa.page_size, pa.num_pages, pa.box, 1))
         return MLA_ERR_CUDA;
     return pl.group_rows == 16
-               ? launch_transposed<16, mla::MlaShape, mla::PagedKv>(pl, tm_q, tm_k, tm_k, a, pa, stream)
-               : launch_transposed<32, mla::MlaShape, mla::PagedKv>(pl, tm_q, tm_k, tm_k, a, pa, stream);
+               ? launch_transposed<16, mla::MlaShape, mla::PagedKv>(pl, tm_q, tm_k, tm_k, a, pa, stream, overlap)
+               : launch_transposed<32, mla::MlaShape, mla::PagedKv>(pl, tm_q, tm_k, tm_k, a, pa, stream, overlap);
 }
 
 mla::CombineArgs combine_args(const mla::MainArgs& a) {
@@ -228,7 +235,7 @@ mla_status run_mla_paged(const mla_plan& pl, const void* q, const void* kv_pages
         return st;
     }
     return launch_dependent(mla::mla_decode_combine_kernel<mla::kDv, mla::PagedKv>, combine_grid(pl),
-                            mla::kCombineThreads, stream, combine_args(a), pa);
+                            mla::kCombineThreads, stream, 0, combine_args(a), pa);
 }
 
 }  // namespace
@@ -317,7 +324,7 @@ mla_status mla_decode_run_paged_fp8(const mla_plan* plan, const void* q, const v
         return st;
     }
     return launch_dependent(mla::mla_decode_combine_kernel<mla::kDv, mla::PagedKv>, combine_grid(pl),
-                            mla::kCombineThreads, stream, combine_args(a), pa);
+                            mla::kCombineThreads, stream, 0, combine_args(a), pa);
 }
 
 mla_status mha_decode_plan_paged(int32_t B, int32_t Sq, int32_t H, int32_t Hkv, int32_t L_max, int32_t page_size,
@@ -377,7 +384,7 @@ mla_status mha_decode_run_paged(const mla_plan* plan, const void* q, const void*
         return st;
     }
     return launch_dependent(mla::mla_decode_combine_kernel<kMhaD, mla::PagedKv>, combine_grid(pl),
-                            mla::kCombineThreads, stream, combine_args(a), pa);
+                            mla::kCombineThreads, stream, 0, combine_args(a), pa);
 }
 
 mla_status mla_decode_plan_prefix(int32_t B, int32_t Sq, int32_t H, int32_t L_max, int32_t prefix_max,
@@ -450,19 +457,21 @@ mla_status mla_decode_run_prefix(const mla_plan* plan, const void* q, const void
     mla::PagedArgs pp = paged_args(pre, prefix_len, prefix_table, 0, num_pages, true);
     pp.len_stride = 0;
     pp.whole_slot = 2 * pl.prefix_partitions;
+    pp.cut_tiles = kPartialCutTiles;
     st = launch_mla_paged(enc, pre, q, q_rows, kv_pages, ap, pp,
                           128ull * (2ull * pl.prefix_partitions + pl.prefix_groups), stream);
     if (st != MLA_OK) {
         cudaGetLastError();
         return st;
     }
-    // the sequences' own keys
+    // the sequences' own keys, on the SMs that the prefix's launch leaves
     mla::MainArgs ao;
     main_args(ao, pl, seqlens, softmax_scale, nullptr, out, lse, workspace, lay.own_lse, lay.own_o);
     mla::PagedArgs po = paged_args(pl, seqlens, block_table, table_stride, num_pages, pl.kernel == MLA_KERNEL_PAIR);
     po.whole_slot = 2 * pl.num_partitions;
+    po.cut_tiles = kPartialCutTiles;
     st = launch_mla_paged(enc, pl, q, q_rows, kv_pages, ao, po,
-                          static_cast<uint64_t>(R) * (2ull * pl.num_partitions + pl.B), stream);
+                          static_cast<uint64_t>(R) * (2ull * pl.num_partitions + pl.B), stream, true);
     if (st != MLA_OK) {
         cudaGetLastError();
         return st;
@@ -481,7 +490,7 @@ mla_status mla_decode_run_prefix(const mla_plan* plan, const void* q, const void
     c.pre_o = ap.part_o;
     c.pre_lse = ap.part_lse;
     c.sinks = sinks;
-    return launch_dependent(mla::mla_prefix_combine_kernel, combine_grid(pl), mla::kCombineThreads, stream, c, po, pp);
+    return launch_dependent(mla::mla_prefix_combine_kernel, combine_grid(pl), mla::kCombineThreads, stream, 0, c, po, pp);
 }
 
 }  // extern "C"

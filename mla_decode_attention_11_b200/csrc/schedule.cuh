@@ -58,14 +58,6 @@ __device__ __forceinline__ long long num_units(int L, int S) {
     return S > 0 ? (n + S - 1) / S : n;
 }
 
-// Where the schedule's functions take a sequence's number of keys from (a
-// callable b -> keys).  SeqLens: an array of lengths on the device.
-struct SeqLens {
-    const int32_t* seqlens;
-    int L_max;
-    __device__ __forceinline__ int operator()(int b) const { return clamp_len(__ldg(seqlens + b), L_max, nullptr); }
-};
-
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -83,7 +75,17 @@ __device__ __forceinline__ long long warp_sum_ll(long long v) {
 // partitions busy, and the longest sequence is no longer than the balanced
 // share plus two cuts, each sequence is one piece (returned as a chunk size
 // covering the longest sequence).
-constexpr long long kCutTiles = 5;
+constexpr int kCutTiles = 5;
+
+// Where the schedule's functions take a sequence's number of keys from (a
+// callable b -> keys, with the cost of a cut in tiles).  SeqLens: an array of
+// lengths on the device.
+struct SeqLens {
+    const int32_t* seqlens;
+    int L_max;
+    __device__ __forceinline__ int operator()(int b) const { return clamp_len(__ldg(seqlens + b), L_max, nullptr); }
+    __device__ __forceinline__ int cut() const { return kCutTiles; }
+};
 
 struct ScheduleScan {
     int S;             // chunk size in tiles of this run's schedule (0: balanced over tiles)
@@ -92,10 +94,10 @@ struct ScheduleScan {
 };
 
 // The chunk size of a run whose plan leaves the choice (0: balanced).
-__device__ __forceinline__ int pick_schedule(long long total, long long n_max, long long nonempty, int P) {
+__device__ __forceinline__ int pick_schedule(long long total, long long n_max, long long nonempty, int P, int cut) {
     if (n_max == 0 || nonempty > P || 2 * nonempty < P) return 0;
     const long long T = (total + P - 1) / P;
-    return n_max <= T + 2 * kCutTiles ? static_cast<int>(n_max) : 0;
+    return n_max <= T + 2 * cut ? static_cast<int>(n_max) : 0;
 }
 
 // One pass over the lengths (warp-cooperative): the schedule of this run, its
@@ -134,7 +136,7 @@ __device__ inline ScheduleScan schedule_scan_warp(const Lens& lens, int B, int P
         n_max = y > n_max ? y : n_max;
     }
     if (plan_split > 0) return {plan_split, chunks, at_chunks};
-    const int S = pick_schedule(total, n_max, nonempty, P);
+    const int S = pick_schedule(total, n_max, nonempty, P, lens.cut());
     if (S > 0) return {S, nonempty, at_nonempty};
     return {0, total, at_tiles};
 }
