@@ -566,10 +566,28 @@ def _stream_on(device: int, stream) -> int:
     return _raw_stream(device) if stream is None and _raw_stream is not None else _stream_handle(stream)
 
 
-def _check_table(t: torch.Tensor, name: str, rows: Optional[int]) -> None:
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """The tensor's device, which has to be the current one."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    return device
+
+
+def _check_on(t: torch.Tensor, name: str, dtype, shape, device: int) -> None:
+    """_check_tensor, and that the tensor is on `device`."""
+    if t.get_device() == device and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return
+    _check_tensor(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, which is not the current device")
+
+
+def _check_table(t: torch.Tensor, name: str, rows: Optional[int], device: int) -> None:
     shape = t.shape
-    if (t.is_cuda and t.dtype == torch.int32 and len(shape) == (1 if rows is None else 2) and shape[-1] > 0 and
-            (rows is None or shape[0] == rows) and (shape[-1] == 1 or t.stride()[-1] == 1)):
+    if (t.get_device() == device and t.dtype == torch.int32 and len(shape) == (1 if rows is None else 2) and
+            shape[-1] > 0 and (rows is None or shape[0] == rows) and (shape[-1] == 1 or t.stride()[-1] == 1)):
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -578,33 +596,30 @@ def _check_table(t: torch.Tensor, name: str, rows: Optional[int]) -> None:
     if t.dim() != (1 if rows is None else 2) or (rows is not None and shape[0] != rows) or shape[-1] < 1:
         raise ValueError(f"{name} must have shape {'(width,)' if rows is None else f'({rows}, width)'}, "
                          f"got {tuple(shape)}")
-    raise ValueError(f"{name}: the entries of a row must be contiguous")
+    if shape[-1] > 1 and t.stride()[-1] != 1:
+        raise ValueError(f"{name}: the entries of a row must be contiguous")
+    raise ValueError(f"{name} is on {t.device}, which is not the current device")
 
 
-def _check_device(device: int, tensors) -> None:
-    """Every tensor is on `device`, and it is the current one."""
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"all tensors must be on cuda:{device}, got {t.device}")
-    if device != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on cuda:{device}, which is not the current device")
+def _check_workspace(workspace: torch.Tensor, device: int) -> None:
+    if workspace.get_device() != device:
+        raise ValueError(f"workspace is on {workspace.device}, which is not the current device")
 
 
 def _check_paged(plan, q, pages, seqlens, block_table, out, lse, sinks, workspace, d_key, d_value, page_row,
                  dtype=torch.bfloat16):
-    """Checks what the paged decodes share; the device's index."""
-    B, Sq, H = plan.B, plan.Sq, plan.H
-    _check_tensor(q, "q", torch.bfloat16, (B, Sq, H, d_key))
+    """Checks what the paged decodes share; the current device's index."""
+    device, B, Sq, H = _device_of(q, "q"), plan.B, plan.Sq, plan.H
+    _check_on(q, "q", torch.bfloat16, (B, Sq, H, d_key), device)
     for name, p in pages:
-        _check_tensor(p, name, dtype, (p.shape[0], plan.page_size, *page_row))
-    _check_tensor(seqlens, "seqlens", torch.int32, (B,))
-    _check_table(block_table, "block_table", B)
-    _check_tensor(out, "out", torch.bfloat16, (B, Sq, H, d_value))
-    _check_tensor(lse, "lse", torch.float32, (B, Sq, H))
+        _check_on(p, name, dtype, (p.shape[0], plan.page_size, *page_row), device)
+    _check_on(seqlens, "seqlens", torch.int32, (B,), device)
+    _check_table(block_table, "block_table", B, device)
+    _check_on(out, "out", torch.bfloat16, (B, Sq, H, d_value), device)
+    _check_on(lse, "lse", torch.float32, (B, Sq, H), device)
     if sinks is not None:
-        _check_tensor(sinks, "sinks", torch.float32, (H,))
-    device = q.get_device()
-    _check_device(device, (seqlens, block_table, out, lse, sinks, workspace, *[p for _, p in pages]))
+        _check_on(sinks, "sinks", torch.float32, (H,), device)
+    _check_workspace(workspace, device)
     return device
 
 
@@ -673,9 +688,8 @@ def mla_decode_run_prefix(plan: mla_plan, q: torch.Tensor, kv_pages: torch.Tenso
     sequences' own keys (the query tokens' among them), found in block_table."""
     device = _check_paged(plan, q, (("kv_pages", kv_pages),), seqlens, block_table, out, lse, sinks, workspace,
                           D_QK, D_V, (D_QK,))
-    _check_table(prefix_table, "prefix_table", None)
-    _check_tensor(prefix_len, "prefix_len", torch.int32, (1,))
-    _check_device(device, (prefix_table, prefix_len))
+    _check_table(prefix_table, "prefix_table", None, device)
+    _check_on(prefix_len, "prefix_len", torch.int32, (1,), device)
     rc = load_library().mla_decode_run_prefix(ctypes.byref(plan), q.data_ptr(), kv_pages.data_ptr(), kv_pages.shape[0],
                                               prefix_table.data_ptr(), prefix_table.shape[0], prefix_len.data_ptr(),
                                               block_table.data_ptr(), block_table.stride(0), block_table.shape[1],
@@ -698,58 +712,65 @@ def rope_table(num_positions: int, dim: int, base: float = 10000.0, device=None)
 _APPEND = struct.Struct("=10iq10Q8qQfi")  # the fields of mla_append, in order
 
 
-def _check_rows(t: torch.Tensor, name: str, shape) -> None:
-    """bf16 rows [T, (heads,) width]: any strides but the last."""
-    if t.is_cuda and t.dtype == torch.bfloat16 and t.shape == shape and t.stride()[-1] == 1:
-        return
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name}: the last dimension must be contiguous")
-
-
-def _strides(t: Optional[torch.Tensor]) -> Tuple[int, int]:
-    """(token, head) element strides; 0 where there is one token or head (or no head axis)."""
-    if t is None:
-        return 0, 0
-    shape, stride = t.shape, t.stride()
+def _rows(t: torch.Tensor, name: str, shape, device: int) -> Tuple[int, int]:
+    """Checks bf16 rows [T, (heads,) width] of any strides but the last; their (token, head) element strides, 0 where
+    there is one token or head (or no head axis)."""
+    stride = t.stride()
+    if not (t.get_device() == device and t.dtype == torch.bfloat16 and t.shape == shape and stride[-1] == 1):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if stride[-1] != 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
     return (stride[0] if shape[0] > 1 else 0), (stride[1] if len(shape) == 3 and shape[1] > 1 else 0)
 
 
-def _append(name, k, v, cos_sin, k_pages, v_pages, block_table, seqlens, cu_tokens, q_in, q_out, q_out_offset,
-            kv_scale, interleaved, workspace, stream, Hkv):
-    T, B = k.shape[0], seqlens.shape[0]
-    _check_tensor(seqlens, "seqlens", torch.int32, (B,))
-    _check_table(block_table, "block_table", B)
-    _check_tensor(cos_sin, "cos_sin", torch.float32, cos_sin.shape)
-    if cos_sin.dim() != 2:
-        raise ValueError(f"cos_sin must have shape (positions, rotated columns), got {tuple(cos_sin.shape)}")
-    if cu_tokens is not None:
-        _check_tensor(cu_tokens, "cu_tokens", torch.int32, (B + 1,))
-    H, out_strides = 0, _strides(q_out)
-    if q_in is not None:
-        H = q_in.shape[1]
-        if (T > 1 and out_strides[0] == 0) or (H > 1 and out_strides[1] == 0):
-            raise ValueError("the rotated queries' rows must not share memory")
-    elif q_out is not None:
+def _query_rows(q_in, q_out, in_name, out_name, T, width, out_width, device):
+    """Heads of the queries to rotate (0: none), and the strides of their rows."""
+    if q_in is None and q_out is None:
+        return 0, (0, 0), (0, 0)
+    if q_in is None or q_out is None:
         raise ValueError("rotated queries need both their input and their output")
-    device = k.get_device()
-    _check_device(device, (v, cos_sin, k_pages, v_pages, block_table, seqlens, cu_tokens, q_in, q_out, workspace))
+    H = q_in.shape[1] if q_in.dim() == 3 else -1
+    in_strides = _rows(q_in, in_name, (T, H, width), device)
+    out_strides = _rows(q_out, out_name, (T, H, out_width), device)
+    if (T > 1 and out_strides[0] == 0) or (H > 1 and out_strides[1] == 0):
+        raise ValueError("the rotated queries' rows must not share memory")
+    return H, in_strides, out_strides
+
+
+def _append(name, device, T, H, Hkv, k, v, cos_sin, k_pages, v_pages, block_table, seqlens, cu_tokens, q_in, q_out,
+            q_out_offset, strides, kv_scale, interleaved, workspace, stream):
+    B = seqlens.shape[0]
+    _check_on(seqlens, "seqlens", torch.int32, (B,), device)
+    _check_table(block_table, "block_table", B, device)
     positions, rot = cos_sin.shape
+    _check_on(cos_sin, "cos_sin", torch.float32, (positions, rot), device)
+    if cu_tokens is not None:
+        _check_on(cu_tokens, "cu_tokens", torch.int32, (B + 1,), device)
+    if workspace is not None:
+        _check_workspace(workspace, device)
     pages, page_size = k_pages.shape[:2]
     args = _APPEND.pack(
         B, T, H, Hkv, rot, 1 if interleaved else 0, positions, page_size, pages, block_table.shape[1],
         block_table.stride()[0], cu_tokens.data_ptr() if cu_tokens is not None else 0, seqlens.data_ptr(),
         block_table.data_ptr(), cos_sin.data_ptr(), k.data_ptr(), v.data_ptr(), q_in.data_ptr() if H else 0,
         q_out.data_ptr() + q_out_offset if H else 0, k_pages.data_ptr(),
-        v_pages.data_ptr() if v_pages is not None else 0, *_strides(k), *_strides(v), *_strides(q_in), *out_strides,
+        v_pages.data_ptr() if v_pages is not None else 0, *strides,
         workspace.data_ptr() if workspace is not None else 0, kv_scale, 0)
     rc = getattr(load_library(), name)(args, _stream_on(device, stream))
     if rc != MLA_OK:
         raise MlaError(rc, name)
+
+
+def _check_cos_sin(cos_sin: torch.Tensor, columns: Optional[int]) -> None:
+    if cos_sin.dim() != 2 or (columns is not None and cos_sin.shape[1] != columns):
+        raise ValueError(f"cos_sin must have shape (positions, {columns or 'rotated columns'}), "
+                         f"got {tuple(cos_sin.shape)}")
 
 
 def mla_cache_append(latent: torch.Tensor, k_rope: torch.Tensor, cos_sin: torch.Tensor, kv_pages: torch.Tensor,
@@ -767,25 +788,20 @@ def mla_cache_append(latent: torch.Tensor, k_rope: torch.Tensor, cos_sin: torch.
     (None: T / B tokens each).  With a decode workspace, tokens without a
     position or page are reported by mla_decode_check.  A contiguous cache
     [B, L_max, 576] is a paged one with block_table[b] = [b]."""
-    T = latent.shape[0]
-    _check_rows(latent, "latent", (T, D_V))
-    _check_rows(k_rope, "k_rope", (T, D_QK - D_V))
+    device, T = _device_of(latent, "latent"), latent.shape[0]
+    k_strides = _rows(latent, "latent", (T, D_V), device)
+    v_strides = _rows(k_rope, "k_rope", (T, D_QK - D_V), device)
     fp8 = kv_pages.dtype in (torch.uint8, torch.float8_e4m3fn)
     if fp8 != (kv_scale is not None):
         raise ValueError("kv_scale goes with a cache of E4M3 codes (torch.uint8 or torch.float8_e4m3fn)")
     if fp8 and not kv_scale > 0:
         raise ValueError("kv_scale must be positive")
-    pages = _fp8_codes(kv_pages) if fp8 else kv_pages
-    _check_tensor(pages, "kv_pages", torch.uint8 if fp8 else torch.bfloat16, (*pages.shape[:2], D_QK))
-    if cos_sin.shape[-1] != D_QK - D_V:
-        raise ValueError(f"cos_sin must have shape (positions, {D_QK - D_V}), got {tuple(cos_sin.shape)}")
-    if q_rope is not None:
-        if q is None:
-            raise ValueError("rotated queries need both their input and their output")
-        _check_rows(q_rope, "q_rope", (T, q_rope.shape[1] if q_rope.dim() == 3 else -1, D_QK - D_V))
-        _check_rows(q, "q", (T, q_rope.shape[1], D_QK))
-    _append("mla_cache_append", latent, k_rope, cos_sin, pages, None, block_table, seqlens, cu_tokens, q_rope, q,
-            2 * D_V, float(kv_scale) if fp8 else 0.0, interleaved, workspace, stream, 1)
+    _check_on(kv_pages, "kv_pages", kv_pages.dtype if fp8 else torch.bfloat16, (*kv_pages.shape[:2], D_QK), device)
+    _check_cos_sin(cos_sin, D_QK - D_V)
+    H, in_strides, out_strides = _query_rows(q_rope, q, "q_rope", "q", T, D_QK - D_V, D_QK, device)
+    _append("mla_cache_append", device, T, H, 1, latent, k_rope, cos_sin, kv_pages, None, block_table, seqlens,
+            cu_tokens, q_rope, q, 2 * D_V, (*k_strides, *v_strides, *in_strides, *out_strides),
+            float(kv_scale) if fp8 else 0.0, interleaved, workspace, stream)
 
 
 def mha_cache_append(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor, k_pages: torch.Tensor,
@@ -798,15 +814,12 @@ def mha_cache_append(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor, k_
     q_in [T, H, 128] into q_out (which may be q_in).  cos_sin: fp32 [positions,
     n], n a multiple of 16 up to 128: the first n columns turn, the rest is
     copied.  Other arguments as mla_cache_append."""
-    T, Hkv = k.shape[0], k.shape[1] if k.dim() == 3 else -1
-    _check_rows(k, "k", (T, Hkv, MHA_D))
-    _check_rows(v, "v", (T, Hkv, MHA_D))
-    _check_tensor(k_pages, "k_pages", torch.bfloat16, (*k_pages.shape[:2], Hkv, MHA_D))
-    _check_tensor(v_pages, "v_pages", torch.bfloat16, k_pages.shape)
-    if q_in is not None:
-        if q_out is None:
-            raise ValueError("rotated queries need both their input and their output")
-        _check_rows(q_in, "q_in", (T, q_in.shape[1] if q_in.dim() == 3 else -1, MHA_D))
-        _check_rows(q_out, "q_out", q_in.shape)
-    _append("mha_cache_append", k, v, cos_sin, k_pages, v_pages, block_table, seqlens, cu_tokens, q_in, q_out, 0, 0.0,
-            interleaved, workspace, stream, Hkv)
+    device, T, Hkv = _device_of(k, "k"), k.shape[0], k.shape[1] if k.dim() == 3 else -1
+    k_strides = _rows(k, "k", (T, Hkv, MHA_D), device)
+    v_strides = _rows(v, "v", (T, Hkv, MHA_D), device)
+    _check_on(k_pages, "k_pages", torch.bfloat16, (*k_pages.shape[:2], Hkv, MHA_D), device)
+    _check_on(v_pages, "v_pages", torch.bfloat16, k_pages.shape, device)
+    _check_cos_sin(cos_sin, None)
+    H, in_strides, out_strides = _query_rows(q_in, q_out, "q_in", "q_out", T, MHA_D, MHA_D, device)
+    _append("mha_cache_append", device, T, H, Hkv, k, v, cos_sin, k_pages, v_pages, block_table, seqlens, cu_tokens,
+            q_in, q_out, 0, (*k_strides, *v_strides, *in_strides, *out_strides), 0.0, interleaved, workspace, stream)
