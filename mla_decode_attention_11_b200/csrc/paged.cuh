@@ -41,7 +41,8 @@ struct PagedArgs {
     int box, box_log2;         // rows per TMA box
     int cut_tiles;             // the schedule's cost of a cut (schedule.cuh)
     int Sq;                    // query tokens (positions count back from L)
-    int window, first;         // window 0: no window
+    int window, first;         // no window: 2^30, which no length reaches, and 0
+    int split;                 // first rounded up to a box
     int heads_log2;            // query rows per token (latent caches: H, a power of two)
     // a shared prefix in front of every sequence's own keys, or null
     const int32_t* prefix_table;
@@ -62,28 +63,19 @@ struct SeqView {
 __device__ __forceinline__ SeqView view_of(const PagedArgs& a, int L) {
     SeqView v;
     v.L = L;
-    v.rows = L;
-    v.split = v.jump = v.lo = 0;
-    v.f = a.first;
     if (a.prefix_table) {
         const int P = clamp_len(__ldg(a.prefix_len), a.prefix_max, nullptr);
         v.f = P;
         v.split = v.lo = ((P + a.box - 1) >> a.box_log2) << a.box_log2;
         v.jump = -v.split;
         v.rows = L > 0 ? v.split + L : P;
-    } else if (a.window > 0) {
-        const int lo = L - a.Sq + 1 - a.window;
-        if (lo > 0) {
-            const int split = ((a.first + a.box - 1) >> a.box_log2) << a.box_log2;
-            const int at = (lo >> a.box_log2) << a.box_log2;
-            v.lo = lo;
-            if (at > split) {
-                v.split = split;
-                v.jump = at - split;
-                v.rows = L - v.jump;
-                v.lo = lo - v.jump;
-            }
-        }
+    } else {
+        const int lo = L - a.Sq + 1 - a.window, left_out = (lo & -a.box) - a.split;
+        v.f = a.first;
+        v.split = a.split;
+        v.jump = left_out > 0 ? left_out : 0;
+        v.rows = L - v.jump;
+        v.lo = (lo > 0 ? lo : 0) - v.jump;
     }
     return v;
 }
@@ -109,16 +101,13 @@ struct RowRange {
 __device__ __forceinline__ RowRange token_rows(const PagedArgs& a, const SeqView& v, int t) {
     const int p = v.L - a.Sq + t;
     RowRange r;
-    r.f = 0;
-    r.b0 = 0;
     r.b1 = p + 1 - v.jump;
     if (a.prefix_table) {
         r.f = v.f;
         r.b0 = v.split;
-    } else if (a.window > 0) {
+    } else {
         r.f = a.first < p + 1 ? a.first : p + 1;
-        const int lo = p + 1 - a.window;
-        if (lo > 0) r.b0 = lo - v.jump > 0 ? lo - v.jump : 0;
+        r.b0 = r.b1 - a.window > 0 ? r.b1 - a.window : 0;
     }
     return r;
 }

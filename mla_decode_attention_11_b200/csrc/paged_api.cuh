@@ -94,9 +94,10 @@ mla::PagedArgs paged_args(const mla_plan& pl, const int32_t* seqlens, const int3
     a.box = page_box(pl.page_size, pair ? 64 : 128);
     a.box_log2 = box_log2(a.box);
     a.Sq = pl.Sq;
-    // a window that no sequence can fill leaves nothing out
-    a.window = pl.window >= pl.L_max ? 0 : pl.window;
-    a.first = pl.first_tokens < pl.L_max ? pl.first_tokens : pl.L_max;
+    const bool windowed = pl.window > 0 && pl.window < pl.L_max;  // one that no sequence fills leaves nothing out
+    a.window = windowed ? pl.window : 1 << 30;
+    a.first = !windowed ? 0 : pl.first_tokens < pl.L_max ? pl.first_tokens : pl.L_max;
+    a.split = (a.first + a.box - 1) / a.box * a.box;
     while ((1 << a.heads_log2) < pl.H) ++a.heads_log2;
     a.whole_slot = -1;
     a.cut_tiles = mla::kCutTiles;

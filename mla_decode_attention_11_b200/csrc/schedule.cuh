@@ -58,10 +58,12 @@ __device__ __forceinline__ long long num_units(int L, int S) {
     return S > 0 ? (n + S - 1) / S : n;
 }
 
-__device__ __forceinline__ long long warp_sum_ll(long long v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+// Sum over a warp of values below 2^42, by the warp's 32-bit reductions (ten
+// 64-bit shuffles a sum took most of the scan's time).
+__device__ __forceinline__ long long warp_sum(long long v) {
+    const unsigned lo = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v) & 0xffffu);
+    const unsigned hi = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v >> 16));
+    return (static_cast<long long>(hi) << 16) + lo;
 }
 
 // Schedule actually used for a run (warp-cooperative; every CTA and the
@@ -108,11 +110,11 @@ __device__ __forceinline__ int pick_schedule(long long total, long long n_max, l
 template <class Lens>
 __device__ inline ScheduleScan schedule_scan_warp(const Lens& lens, int B, int P, int plan_split, int b_at = -1) {
     const int lane = threadIdx.x & 31;
-    long long total = 0, n_max = 0, nonempty = 0, chunks = 0;
-    long long at_tiles = 0, at_nonempty = 0, at_chunks = 0;
+    long long total = 0, chunks = 0, at_tiles = 0, at_chunks = 0;
+    int n_max = 0, nonempty = 0, at_nonempty = 0;
     for (int b = lane; b < B; b += 32) {
         const int L = lens(b);
-        const long long n = num_tiles(L);
+        const int n = num_tiles(L);
         const long long c = plan_split > 0 ? num_units(L, plan_split) : 0;
         total += n;
         n_max = n > n_max ? n : n_max;
@@ -124,21 +126,13 @@ __device__ inline ScheduleScan schedule_scan_warp(const Lens& lens, int B, int P
             at_chunks += c;
         }
     }
-    total = warp_sum_ll(total);
-    nonempty = warp_sum_ll(nonempty);
-    chunks = warp_sum_ll(chunks);
-    at_tiles = warp_sum_ll(at_tiles);
-    at_nonempty = warp_sum_ll(at_nonempty);
-    at_chunks = warp_sum_ll(at_chunks);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const long long y = __shfl_xor_sync(0xffffffffu, n_max, o);
-        n_max = y > n_max ? y : n_max;
-    }
-    if (plan_split > 0) return {plan_split, chunks, at_chunks};
+    if (plan_split > 0) return {plan_split, warp_sum(chunks), b_at > 0 ? warp_sum(at_chunks) : 0};
+    total = warp_sum(total);
+    nonempty = __reduce_add_sync(0xffffffffu, nonempty);
+    n_max = __reduce_max_sync(0xffffffffu, n_max);
     const int S = pick_schedule(total, n_max, nonempty, P, lens.cut());
-    if (S > 0) return {S, nonempty, at_nonempty};
-    return {0, total, at_tiles};
+    if (S > 0) return {S, nonempty, b_at > 0 ? __reduce_add_sync(0xffffffffu, at_nonempty) : 0};
+    return {0, total, b_at > 0 ? warp_sum(at_tiles) : 0};
 }
 
 // Locate the first sequence overlapping flat unit `start` (warp-cooperative).
@@ -148,26 +142,24 @@ __device__ inline void locate_warp(const Lens& lens, int B, int S, long long sta
     long long acc = 0;
     for (int base = 0; base < B; base += 32) {
         const int b = base + lane;
-        const long long n = (b < B) ? num_units(lens(b), S) : 0;
-        // inclusive prefix within the warp
-        long long incl = n;
+        const int n = (b < B) ? static_cast<int>(num_units(lens(b), S)) : 0;  // < 2^18
+        const int sum = __reduce_add_sync(0xffffffffu, n);
+        if (acc + sum > start) {
+            // inclusive prefix within the warp
+            int incl = n;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
-        const long long excl = incl - n;
-        // sequences with n > 0 whose range [acc+excl, acc+incl) reaches past start
-        const bool hit = (b < B) && (n > 0) && (acc + incl > start);
-        const unsigned m = __ballot_sync(0xffffffffu, hit);
-        if (m) {
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            // the first sequence with n > 0 whose range [acc + incl - n, acc + incl) reaches past start
+            const unsigned m = __ballot_sync(0xffffffffu, n > 0 && acc + incl > start);
             const int src = __ffs(m) - 1;
-            const long long e = __shfl_sync(0xffffffffu, excl, src);
             *b_out = base + src;
-            *acc_out = acc + e;
+            *acc_out = acc + __shfl_sync(0xffffffffu, incl - n, src);
             return;
         }
-        acc += __shfl_sync(0xffffffffu, incl, 31);
+        acc += sum;
     }
     *b_out = B;
     *acc_out = acc;
