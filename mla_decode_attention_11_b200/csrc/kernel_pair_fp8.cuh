@@ -28,6 +28,10 @@
 // loaded per tile (and the TMA bytes) are half.  The Q terms are written by
 // the softmax warps at the start of each piece (plain loads of the bf16 q);
 // the leader's QK^T issuer waits until both CTAs have written theirs.
+//
+// In pages (CV = PagedKv): as in kernel_pair.cuh, a V slot being [128 / box][2
+// chunks][box rows][64 bytes]; the PV steps take 32 keys, so a box has at least
+// 32 rows.
 #pragma once
 
 #include <cuda.h>
@@ -56,7 +60,7 @@ __device__ __forceinline__ __half2 e4m3x2_to_f16x2(uint32_t codes) {
     return *reinterpret_cast<const __half2*>(&h);
 }
 
-template <int NK, int NV, int NS, int NP>
+template <int NK, int NV, int NS, int NP, bool kPaged = false>
 struct PairFp8Cfg {
     static constexpr int kThreads = 256;
     static constexpr int kRows = 64;                          // query rows per CTA
@@ -78,14 +82,15 @@ struct PairFp8Cfg {
     static constexpr int OFF_RED = OFF_P + NP * kPBuf;         // floats: [2][128] max, [128] sum, [128] q amax, [64] q scale
     static constexpr int OFF_BAR = OFF_RED + 576 * 4;
     // q_full, q_empty, pv_done[NP], drain_s, drain_pv, group_sync, s_full[NS], p_full[NS], p_local[NS],
-    // k_full[NK], k_empty[NK], v_full[NV], v_empty[NV]
-    static constexpr int kNumBars = 6 + NP + 3 * NS + 2 * NK + 2 * NV;
+    // k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], v_here
+    static constexpr int kNumBars = 7 + NP + 3 * NS + 2 * NK + 2 * NV;
     static constexpr int OFF_MISC = OFF_BAR + kNumBars * 8;
-    static constexpr int kSmemBytes = OFF_MISC + 64;
+    static constexpr int OFF_LIST = OFF_MISC + 64;  // paged: box lists of the K and the V producer
+    static constexpr int kSmemBytes = OFF_LIST + (kPaged ? 2 * 512 : 0);
     static constexpr uint32_t kTmemCols = 512;                 // O: [0,256), S buffers from 256, 64 each
     static constexpr uint32_t kColS = 256;
     static_assert(NS >= 2 && 256 + 64 * NS <= 512, "S buffers must fit next to O in TMEM");
-    static_assert(NS <= 4, "one 4-byte forwarding slot per S buffer in the 64-byte misc area (words 12..15)");
+    static_assert(NS <= (kPaged ? 3 : 4), "a 4-byte forwarding slot per S buffer, and one for v_here, in the 64-byte misc area (words 12..15)");
     // kind::f8f6f4 with E4M3 A and B: format codes 0 (the bit layout of the f16 descriptor)
     static constexpr uint32_t kIdescS = ptx::make_idesc_f16(128, 128, 0, 0);
     static constexpr uint32_t kIdescPV = ptx::make_idesc_f16(128, 256, 0, 1);
@@ -108,12 +113,15 @@ __device__ __forceinline__ void mma_e4m3_ss_pair(uint32_t d_tmem, uint64_t a_des
         : "memory");
 }
 
-template <int NK, int NV, int NS, int NP>
+template <int NK, int NV, int NS, int NP, class CV = ContigKv>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     mla_decode_pair_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                                const __grid_constant__ CUtensorMap tm_pf, const __grid_constant__ CUtensorMap tm_out,
-                               const __grid_constant__ CUtensorMap tm_part, const MainArgs args) {
-    using C = PairFp8Cfg<NK, NV, NS, NP>;
+                               const __grid_constant__ CUtensorMap tm_part, const MainArgs args,
+                               const __grid_constant__ typename CV::Args pa) {
+    using C = PairFp8Cfg<NK, NV, NS, NP, CV::kPaged>;
+    using Walker = PieceWalkerOf<typename CV::Lens>;
+    static_assert(!CV::kPaged || NV >= 2, "the V slots of a whole tile are resident while its unseen rows are cleared");
     extern __shared__ __align__(1024) uint8_t smem[];
 
     uint8_t* q_smem = smem + C::OFF_Q;
@@ -137,6 +145,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     uint64_t* k_empty = k_full + NK;
     uint64_t* v_full = k_empty + NK;
     uint64_t* v_empty = v_full + NV;
+    uint64_t* v_here = v_empty + NV;        // paged: this CTA's V slots of a tile with rows to clear have landed
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     uint32_t* tmem_base_slot = misc + 0;
     int* b_first_slot = reinterpret_cast<int*>(misc + 2);
@@ -177,6 +186,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             ptx::mbar_init(v_full + i, 1);
             ptx::mbar_init(v_empty + i, 1);
         }
+        ptx::mbar_init(v_here, 1);
         ptx::fence_mbarrier_init();
         if (!smem_ok) atomicOr(args.status, kStatusTimeout);
     }
@@ -185,13 +195,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         ptx::tmem_relinquish_pair();
     }
     if (warp == 0) {
-        const ScheduleScan sc = schedule_scan_warp(SeqLens{args.seqlens, args.L_max}, args.B, args.P, args.split_tiles);
+        const ScheduleScan sc = schedule_scan_warp(make_lens(args, pa), args.B, args.P, args.split_tiles);
         const int S_eff = sc.S;
         const long long total = sc.units;
         const long long T = (total + args.P - 1) / args.P;
         int bf;
         long long af;
-        locate_warp(SeqLens{args.seqlens, args.L_max}, args.B, S_eff, static_cast<long long>(p) * T, &bf, &af);
+        locate_warp(make_lens(args, pa), args.B, S_eff, static_cast<long long>(p) * T, &bf, &af);
         if (lane == 0) {
             *b_first_slot = bf;
             *acc_first_slot = af;
@@ -217,11 +227,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     // dependent) may start scheduling its CTAs; it waits for this grid's results
     ptx::launch_dependents();
 
-    PieceWalker walker;
+    Walker walker;
     {
         const long long total = *total_slot;
         const long long T = (total + args.P - 1) / args.P;
-        walker.lens = SeqLens{args.seqlens, args.L_max};
+        walker.lens = make_lens(args, pa);
         walker.B = args.B;
         walker.p = p;
         walker.S = *split_slot;
@@ -234,10 +244,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     // shared::cluster address of the leader's Q barrier
     const uint32_t lead_q_full = ptx::mapa_shared(ptx::smem_u32(q_full), 0);
     const bool stall_cta = (blockIdx.x == 0);
+    uint32_t box_rows = kTileKV;
+    if constexpr (CV::kPaged) box_rows = static_cast<uint32_t>(pa.box);
 
     if (warp == 4) {
-        // ============================================================ Q + K producer
-        if (ptx::elect_one()) {
+        // ============================================================ K producer
+        if constexpr (CV::kPaged) {
+            uint32_t k_cnt = 0;
+            int unit = 1;  // (as below, but a later piece's Q has no number)
+            // the boxes of this CTA's 64 rows of a tile
+            BoxList<Walker, 2> boxes(pa, walker, smem + C::OFF_LIST, lane, static_cast<int>(rank) * 64, 6);
+            const uint32_t box_bytes = static_cast<uint32_t>(kChunk) << pa.box_log2;
+            const bool ok = boxes.run(args.status, [&](int tile, bool more) -> bool {
+                if (more && args.prefetch_tiles > 0)  // the next tile into L2, K and V columns alike
+                    boxes.get(tile + 1).each([&](int, int row, int page) {
+                        if (page < pa.num_pages) ptx::tma_prefetch_4d(&tm_pf, 0, row, 0, page);
+                    });
+                const auto box = boxes.get(tile);
+#pragma unroll 3
+                for (int jj = 0; jj < kNumChunks; ++jj) {
+                    const int j = (jj == 0) ? 8 : jj - 1;  // rope chunk first
+                    const uint32_t s = k_cnt % NK;
+                    if (!ptx::mbar_wait_bounded(k_empty + s, ((k_cnt / NK) & 1) ^ 1, tmo)) return false;
+                    if (leader) ptx::mbar_arrive_expect_tx(k_full + s, 2 * C::kKChunk);
+                    if (!(stall_cta && unit == args.stall_unit))
+                        box.each([&](int i, int row, int page) {
+                            ptx::tma_load_3d_pair(k_smem + s * C::kKChunk + i * box_bytes, &tm_k,
+                                                  ptx::mapa_shared(ptx::smem_u32(k_full + s), 0), j * kChunk, row, page);
+                        });
+                    ++unit;
+                    ++k_cnt;
+                }
+                return true;
+            });
+            if (ptx::elect_one()) {
+                if (!ok) atomicOr(args.status, kStatusTimeout);
+                if (leader) {  // every armed load has landed before teardown
+                    bool drained = true;
+                    const uint32_t n_k = k_cnt < static_cast<uint32_t>(NK) ? k_cnt : static_cast<uint32_t>(NK);
+                    for (uint32_t i = 0; i < n_k; ++i) {
+                        const uint32_t c = k_cnt - 1 - i;
+                        drained &= ptx::mbar_wait_bounded(k_full + c % NK, (c / NK) & 1, tmo);
+                    }
+                    if (!drained) atomicOr(args.status, kStatusTimeout);
+                }
+            }
+        } else if (ptx::elect_one()) {
             // K as one 64-code chunk of this CTA's 64 kv rows per slot; the L2
             // prefetch of a tile as one box of 64 rows x all 9 chunks
             uint32_t k_cnt = 0, piece_cnt = 0;
@@ -248,7 +300,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             // is prefetched whole (this CTA's 64 rows, K and V columns alike).
             // The cursor skips the first tile (loaded at once), so nothing
             // queues ahead of the loads the first MMA needs.
-            PieceWalker pf_walker = walker;
+            Walker pf_walker = walker;
             Piece pf_pc{};
             bool pf_live = false, pf_started = false;
             int pf_t = 0;
@@ -311,7 +363,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         __syncwarp();
     } else if (warp == 5) {
         // ============================================================ V producer
-        if (ptx::elect_one()) {
+        if constexpr (CV::kPaged) {
+            uint32_t v_cnt = 0;
+            BoxList<Walker, 4> boxes(pa, walker, smem + C::OFF_LIST + 512, lane, 0, 7);
+            const uint32_t box_bytes = 2u * kChunk << pa.box_log2;  // two chunks
+            const bool ok = boxes.run(args.status, [&](int tile, bool) -> bool {
+                const auto box = boxes.get(tile);
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t s = v_cnt % NV;
+                    if (!ptx::mbar_wait_bounded(v_empty + s, ((v_cnt / NV) & 1) ^ 1, tmo)) return false;
+                    if (leader) ptx::mbar_arrive_expect_tx(v_full + s, 2 * C::kVSlot);
+                    const int col0 = 256 * i + 128 * static_cast<int>(rank);  // two adjacent chunks, one box
+                    box.each([&](int k, int row, int page) {
+                        ptx::tma_load_4d_pair(v_smem + s * C::kVSlot + k * box_bytes, &tm_v,
+                                              ptx::mapa_shared(ptx::smem_u32(v_full + s), 0), 0, row, col0 / kChunk,
+                                              page);
+                    });
+                    ++v_cnt;
+                }
+                return true;
+            });
+            if (ptx::elect_one()) {
+                if (!ok) atomicOr(args.status, kStatusTimeout);
+                if (leader) {
+                    bool drained = true;
+                    const uint32_t n_v = v_cnt < static_cast<uint32_t>(NV) ? v_cnt : static_cast<uint32_t>(NV);
+                    for (uint32_t i = 0; i < n_v; ++i) {
+                        const uint32_t c = v_cnt - 1 - i;
+                        drained &= ptx::mbar_wait_bounded(v_full + c % NV, (c / NV) & 1, tmo);
+                    }
+                    if (!drained) atomicOr(args.status, kStatusTimeout);
+                }
+            }
+        } else if (ptx::elect_one()) {
             uint32_t v_cnt = 0;
             bool ok = true;
             Piece pc;
@@ -434,14 +519,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             // P terms: K-major, 64-byte rows (64 keys); V: MN-major, two 64-column
             // chunks kVChunk apart (LBO), 8-key atoms of 512 bytes (SBO)
             const uint64_t dp0 = ptx::make_smem_desc(ptx::smem_u32(p_smem), 16, 512, ptx::Swizzle::B64);
-            const uint64_t dv0 = ptx::make_smem_desc(ptx::smem_u32(v_smem), C::kVChunk, 512, ptx::Swizzle::B64);
+            // (paged: the next 64 columns are one chunk of a box further)
+            const uint32_t v_chunk = CV::kPaged ? kChunk * box_rows : static_cast<uint32_t>(C::kVChunk);
+            const uint64_t dv0 = ptx::make_smem_desc(ptx::smem_u32(v_smem), v_chunk, 512, ptx::Swizzle::B64);
             uint32_t vs = 0, vph = 0;  // V ring slot and phase
             uint32_t u = 0;            // global tile index
             Piece pc;
             while (ok && walker.next(pc)) {
+                SeqView view{};
+                if constexpr (CV::kPaged) view = view_of(pa, paged_len(pa, pc.b));
                 for (int t = pc.tile_lo; ok && t < pc.tile_hi; ++t) {
                     const bool first = (t == pc.tile_lo);  // O starts over for a new piece
                     const uint32_t pb = (NP == 2) ? (u & 1) : 0;
+                    if constexpr (CV::kPaged) {
+                        if (tile_unseen(pa, view, t)) {
+                            // both of the tile's V slots are here (the loads of both CTAs are counted on
+                            // these barriers): the softmax threads may clear rows in them
+                            const uint32_t second = vs + 1 == NV ? 0 : vs + 1;
+                            ok = ptx::mbar_wait_bounded_cluster(v_full + vs, vph, tmo) &&
+                                 ptx::mbar_wait_bounded_cluster(v_full + second, second ? vph : vph ^ 1, tmo);
+                            if (!ok) break;
+                            ptx::mbar_arrive(v_here);
+                            ptx::st_async_u32(ptx::mapa_shared(ptx::smem_u32(fwd_slot + NS), 1), u,
+                                              ptx::mapa_shared(ptx::smem_u32(v_here), 1));
+                        }
+                    }
                     ok = ptx::mbar_wait_bounded_cluster(p_full + (u % NS), (u / NS) & 1, tmo);
                     if (!ok) break;
                     ptx::tc_fence_after();
@@ -454,11 +556,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                         // 32 keys per MMA (4 steps), both P terms against the same V rows
 #pragma unroll
                         for (int kk = 0; kk < kTileKV / 32; ++kk) {
+                            uint32_t voff = kk * 2048;  // 32 rows of 64 bytes a step
+                            if constexpr (CV::kPaged) {
+                                const uint32_t row = 32u * kk, in_box = row & (box_rows - 1);
+                                voff = (row - in_box) * 128u + in_box * 64u;
+                            }
 #pragma unroll
                             for (int tp = 0; tp < 2; ++tp) {
                                 const uint64_t da =
                                     dpb + ((tp * C::kPTerm + (kk >> 1) * C::kPChunk + (kk & 1) * 32) >> 4);
-                                mma_e4m3_ss_pair(tmem_base + 128 * i, da, db + ((kk * 2048) >> 4), C::kIdescPV,
+                                mma_e4m3_ss_pair(tmem_base + 128 * i, da, db + (voff >> 4), C::kIdescPV,
                                                  (first && kk == 0 && tp == 0) ? 0u : 1u);
                             }
                         }
@@ -484,7 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         const int r = L_id & 63;            // query row within this CTA's 64
         const int h = L_id >> 6;            // which 64 keys of the tile (S), which 128 dv of each N=256 (O)
         const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
-        uint32_t tile_cnt = 0, sync_cnt = 0, piece_cnt = 0;
+        uint32_t tile_cnt = 0, sync_cnt = 0, piece_cnt = 0, here_cnt = 0;
         bool ok = true;
         // scores are scaled by cs before exp2; a non-positive scale is applied to
         // the raw scores up front (cs = 1 after that), so that the row max of the
@@ -594,10 +701,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             const float row_cs = args.scale_log2 * qscale[r];  // score scale of this row (base 2)
             float m_ref = -INFINITY;  // reference max (base 2) of the row, the same in both of its threads
             float l_part = 0.f;       // this thread's share of the row sum (of 2^4 p), relative to m_ref
+            SeqView view{};
+            RowRange seen{};          // paged: the rows this thread's query row sees
+            if constexpr (CV::kPaged) {
+                view = view_of(pa, paged_len(pa, pc.b));
+                seen = token_rows(pa, view, (g * 128 + static_cast<int>(rank) * 64 + r) >> pa.heads_log2);
+            }
             for (int t = pc.tile_lo; t < pc.tile_hi; ++t) {
                 const bool first = (t == pc.tile_lo);
                 int row0 = t * kTileKV;
-                if (row0 + kTileKV > pc.L) row0 = pc.L - kTileKV;
+                if (!CV::kPaged && row0 + kTileKV > pc.L) row0 = pc.L - kTileKV;
                 const int kv0 = row0 + 64 * h;       // key of column j is kv0 + j
                 const int lo = t * kTileKV;          // keys below lo belong to the previous tile
                 const uint32_t buf = tile_cnt % NS;
@@ -624,7 +737,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 }
                 // only the end-aligned last tile of a sequence holds keys of the
                 // previous tile (below lo); every key of a tile is below L
-                if (row0 < lo) {
+                if constexpr (CV::kPaged) {
+                    if (!seen.all(kv0, 64)) {
+                        const uint64_t bits = bits_between(0, seen.f - kv0) | bits_between(seen.b0 - kv0, seen.b1 - kv0);
+                        const uint32_t lo32 = static_cast<uint32_t>(bits), hi32 = static_cast<uint32_t>(bits >> 32);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            if (!(lo32 >> j & 1)) x[j] = -INFINITY;
+                            if (!(hi32 >> j & 1)) x[32 + j] = -INFINITY;
+                        }
+                    }
+                } else if (row0 < lo) {
 #pragma unroll
                     for (int j = 0; j < 64; ++j)
                         if (kv0 + j < lo) x[j] = -INFINITY;
@@ -686,7 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 float alpha = 1.f;
                 bool grow = false;
                 if (first) {
-                    m_ref = mrow;
+                    m_ref = CV::kPaged ? fmaxf(mrow, kNoKey) : mrow;
                     exps(m_ref);
                 } else if (mrow > m_ref + C::kLazy) {
                     grow = true;
@@ -727,6 +850,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                     }
                     ptx::tmem_wait_st();
                 }
+                if constexpr (CV::kPaged) {
+                    // values of rows that no token sees: P is 0 there, and 0 times
+                    // whatever the page holds (a NaN code) must be 0
+                    if (tile_unseen(pa, view, t)) {
+                        if (!leader && L_id == 0) ptx::mbar_arrive_expect_tx(v_here, 4);
+                        ok = ptx::mbar_wait_bounded_cluster(v_here, here_cnt & 1, tmo);
+                        if (!ok) break;
+                        ++here_cnt;
+                        if (unseen(pa, view, row0 + L_id)) {
+                            const uint32_t in_box = static_cast<uint32_t>(L_id) & (box_rows - 1);
+                            const uint32_t at = (L_id - in_box) * 128u + in_box * 64u;
+#pragma unroll 1
+                            for (uint32_t i = 0; i < 2; ++i) {
+                                uint8_t* vrow = v_smem + ((2 * tile_cnt + i) % NV) * C::kVSlot + at;
+                                clear_row<kChunk>(vrow, lane);
+                                clear_row<kChunk>(vrow + box_rows * kChunk, lane);
+                            }
+                        }
+                    }
+                }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     uint8_t* pchunk = p_smem + pb * C::kPBuf + k * C::kPTerm + h * C::kPChunk;
@@ -764,7 +907,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             float o_fac = 1.f;
             if (args.sinks != nullptr && pc.slot < 0)
                 o_fac = fold_sink(m_ref, l_row, args.sinks[qrow % args.H] * kLog2e);
-            const float inv_l = o_fac * args.o_scale * C::kPScaleInv / l_row;
+            const float inv_l = (CV::kPaged && l_row == 0.f) ? 0.f : o_fac * args.o_scale * C::kPScaleInv / l_row;
             if (h == 0) {
                 const float lse_nat = (m_ref + log2f(l_row)) * 0.69314718055994530942f;
                 if (pc.slot < 0)

@@ -167,15 +167,20 @@ mla_status launch_pair(const mla_plan& plan, const CUtensorMap& tm_q, const CUte
 constexpr int kPairFp8NK = 18;  // K chunks of 4 KB (two tiles)
 constexpr int kPairFp8NV = 3;   // V slots of 16 KB (a tile and a half)
 using PairFp8C = mla::PairFp8Cfg<kPairFp8NK, kPairFp8NV, kPairNS, kPairNP>;
+constexpr int kPairFp8PagedNK = 17;  // one chunk fewer: the producers' box lists
+using PairFp8PagedC = mla::PairFp8Cfg<kPairFp8PagedNK, kPairFp8NV, kPairNS, kPairNP, true>;
 
+template <class CV = mla::ContigKv>
 mla_status launch_pair_fp8(const mla_plan& plan, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                            const CUtensorMap& tm_pf, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
-                           const mla::MainArgs& args, cudaStream_t stream) {
-    auto kern = mla::mla_decode_pair_fp8_kernel<kPairFp8NK, kPairFp8NV, kPairNS, kPairNP>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairFp8C::kSmemBytes) != cudaSuccess)
+                           const mla::MainArgs& args, const typename CV::Args& pa, cudaStream_t stream) {
+    constexpr int kNK = CV::kPaged ? kPairFp8PagedNK : kPairFp8NK;
+    constexpr int kSmem = CV::kPaged ? PairFp8PagedC::kSmemBytes : PairFp8C::kSmemBytes;
+    auto kern = mla::mla_decode_pair_fp8_kernel<kNK, kPairFp8NV, kPairNS, kPairNP, CV>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
         return MLA_ERR_CUDA;
     const dim3 grid(static_cast<unsigned>(2 * plan.num_partitions * plan.num_groups));
-    kern<<<grid, PairFp8C::kThreads, PairFp8C::kSmemBytes, stream>>>(tm_k, tm_v, tm_pf, tm_out, tm_part, args);
+    kern<<<grid, PairFp8C::kThreads, kSmem, stream>>>(tm_k, tm_v, tm_pf, tm_out, tm_part, args, pa);
     return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
@@ -574,7 +579,7 @@ mla_status launch_phases(const mla_plan& pl, const void* q, const void* kv, cons
         if (pl.kernel == MLA_KERNEL_PAIR)
             st = launch_pair(pl, tm_q, tm_k, tm_kv, tm_pf, tm_out, tm_part, a, {}, stream);
         else if (pl.kernel == MLA_KERNEL_FP8_PAIR)
-            st = launch_pair_fp8(pl, tm_k, tm_kv, tm_pf, tm_out, tm_part, a, stream);
+            st = launch_pair_fp8(pl, tm_k, tm_kv, tm_pf, tm_out, tm_part, a, {}, stream);
         else if (pl.kernel == MLA_KERNEL_FP8_MMA)
             st = (G == 16) ? launch_fp8mma<16>(pl, tm_kv, a, {}, stream) : launch_fp8mma<32>(pl, tm_kv, a, {}, stream);
         else if (fp8)

@@ -276,10 +276,14 @@ mla_status mla_decode_plan_paged_fp8(int32_t B, int32_t Sq, int32_t H, int32_t L
                                      int32_t num_partitions_override, mla_plan* plan, size_t* workspace_bytes) {
     if (!plan) return MLA_ERR_INVALID_ARG;
     mla_plan p;
-    mla_status st = mla_decode_plan_fp8_kernel(B, Sq, H, L_max, device, num_partitions_override, MLA_KERNEL_FP8_MMA, &p,
-                                               nullptr);
+    // the CTA-pair kernel as for a contiguous cache, where a page divides into
+    // boxes of 32 rows; the transposed operand kernel takes any
+    const int32_t kernel = page_size % 32 == 0 ? 0 : MLA_KERNEL_FP8_MMA;
+    mla_status st =
+        mla_decode_plan_fp8_kernel(B, Sq, H, L_max, device, num_partitions_override, kernel, &p, nullptr);
     if (st == MLA_OK) st = check_page_args(page_size, window, first_tokens);
     if (st != MLA_OK) return st;
+    if (p.kernel == MLA_KERNEL_FP8_PAIR) p.smem_bytes = PairFp8PagedC::kSmemBytes;
     p.page_size = page_size;
     p.window = window;
     p.first_tokens = first_tokens;
@@ -298,8 +302,10 @@ mla_status mla_decode_run_paged_fp8(const mla_plan* plan, const void* q, const v
     if (st != MLA_OK) return st;
     const mla_plan& pl = *plan;
     const int R = pl.Sq * pl.H, G = pl.group_rows;
-    if (pl.kernel != MLA_KERNEL_FP8_MMA || pl.Hkv != 1 || pl.head_dim != mla::kDqk || (G != 16 && G != 32) ||
-        G * pl.num_groups != R || pl.prefix_max != 0 || !(std::isfinite(kv_scale) && kv_scale > 0.f))
+    const bool pair = pl.kernel == MLA_KERNEL_FP8_PAIR;
+    if (!(pair ? G == 128 && pl.page_size % 32 == 0 : pl.kernel == MLA_KERNEL_FP8_MMA && (G == 16 || G == 32)) ||
+        pl.Hkv != 1 || pl.head_dim != mla::kDqk || G * pl.num_groups != R || pl.prefix_max != 0 ||
+        !(std::isfinite(kv_scale) && kv_scale > 0.f))
         return MLA_ERR_INVALID_ARG;
     const Layout lay = workspace_layout(num_slots(pl), R);
     if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
@@ -313,7 +319,23 @@ mla_status mla_decode_run_paged_fp8(const mla_plan* plan, const void* q, const v
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * kv_scale * 1.4426950408889634074);
     a.o_scale = kv_scale;
-    mla::PagedArgs pa = paged_args(pl, seqlens, block_table, table_stride, num_pages, false);
+    mla::PagedArgs pa = paged_args(pl, seqlens, block_table, table_stride, num_pages, pair);
+    if (pair) {
+        CUtensorMap tm_k, tm_v, tm_pf, tm_out, tm_part;
+        if (!encode_kv_fp8(enc, &tm_k, kv_pages, pl.page_size, num_pages, pa.box) ||
+            !encode_kv_fp8_chunks(enc, &tm_v, kv_pages, pl.page_size, num_pages, pa.box, 2) ||
+            !encode_kv_fp8_chunks(enc, &tm_pf, kv_pages, pl.page_size, num_pages, pa.box, mla::kNumChunks) ||
+            !encode_rows_store(enc, &tm_out, out, static_cast<uint64_t>(pl.B) * R, false) ||
+            !encode_rows_store(enc, &tm_part, a.part_o, static_cast<uint64_t>(num_slots(pl)) * R, true))
+            return MLA_ERR_CUDA;
+        st = launch_pair_fp8<mla::PagedKv>(pl, tm_k, tm_v, tm_pf, tm_out, tm_part, a, pa, stream);
+        if (st != MLA_OK) {
+            cudaGetLastError();
+            return st;
+        }
+        return launch_dependent(mla::mla_decode_combine_kernel<mla::kDv, mla::PagedKv>, combine_grid(pl),
+                                mla::kCombineThreads, stream, 0, combine_args(a), pa);
+    }
     CUtensorMap tm_kv;
     if (!encode_kv_fp8(enc, &tm_kv, kv_pages, pl.page_size, num_pages, pa.box) ||
         !encode_kv_fp8_chunks(enc, &pa.prefetch, kv_pages, pl.page_size, num_pages, pa.box, mla::kNumChunks))

@@ -5,9 +5,12 @@ a plain implementation in 64 bits on the same inputs, and of their refusals.
 Tolerances.  Scores accumulate n products of the key's width in fp32, so each is off by at most
 n 2^-24 scale sum |q k| =: delta (first order), and so is lse; its sum and its logarithm add a few 2^-23 of its value.
 The weights a row multiplies its values with are rounded to bf16 (2^-8 relative; E4M3 pages: two E4M3 terms, 2^-4 of
-2^-4, and 2^-14 of the largest weight where the second term has no more bits), so with A = sum p |v| an output is off
+2^-4, of a weight rounded to f16 at most, 2^-11, and 2^-14 of the largest weight where the second term has no more
+bits), so with A = sum p |v| an output is off
 by at most (2^-8 + 2 delta) A, and by 2^-8 of itself from its own rounding.  2^-20 stands for the fp32 steps of the
-merges.  Rows of a page that no token sees hold NaN (or the NaN code), and so do outputs before a call.
+merges.  E4M3 pages: a query row, scaled so that its largest element is in [224, 448], is carried as two or three E4M3
+terms.  Two hold the 8 bits of a bf16 exactly unless its last bit is below E4M3's smallest step 2^-9, and are off by half
+of that otherwise: 2^-10 / 224 of the row's largest element, in each of the products.  Rows of a page that no token sees hold NaN (or the NaN code), and so do outputs before a call.
 """
 import math
 
@@ -98,6 +101,9 @@ def reference(q, seqs, masks, scale, sinks, values):
         s = torch.einsum("thgd,nhd->thgn", qq, k) * scale
         s = torch.where(seen, s, -math.inf)
         delta = torch.einsum("thgd,nhd->thgn", qq.abs(), k.abs()) * (abs(scale) * D * 2.0 ** -24)
+        if reference.fp8:
+            delta = delta + torch.einsum("thgd,nhd->thgn", qq.abs().amax(-1, keepdim=True).expand_as(qq), k.abs()) * (
+                abs(scale) * 2.0 ** -10 / 224)
         delta = torch.where(seen, delta, 0.0).amax(-1) if n else torch.zeros(Sq, Hkv, gq, device=DEV).double()
         sk = None if sinks is None else sinks.double().view(1, Hkv, gq, 1).expand(Sq, Hkv, gq, 1)
         full = s if sk is None else torch.cat([s, sk], -1)
@@ -111,7 +117,7 @@ def reference(q, seqs, masks, scale, sinks, values):
         d = delta[..., None]
         # E4M3 weights: 2^-14 of the row's largest weight, at most p.max(), for each key
         small = p.amax(-1, keepdim=True) * torch.einsum("thgn,nhd->thgd", seen.double(), v.abs()) if n else a
-        tol_o[b] = ((2.0 ** -8 + 2 * d + 2.0 ** -20) * a + 2.0 ** -8 * o.abs() + 2.0 ** -14 * small * reference.fp8
+        tol_o[b] = ((2.0 ** -8 + 2.0 ** -11 * reference.fp8 + 2 * d + 2.0 ** -20) * a + 2.0 ** -8 * o.abs() + 2.0 ** -14 * small * reference.fp8
                     ).reshape(Sq, H, values)
         tol_l[b] = torch.where(l == -math.inf, 0.0, delta + 2.0 ** -20 * (1 + l.abs())).reshape(Sq, H)
     return out, lse, tol_o, tol_l
@@ -212,7 +218,7 @@ def test_window_mla_tokens(cuda_device, Sq, H, page, window, first):
 @pytest.mark.parametrize("parts", [0, 1, 7])
 @pytest.mark.parametrize("window,first", [(0, 0), (1, 1), (40, 5), (200, 16)])
 @pytest.mark.parametrize("page", [16, 96, 128])
-@pytest.mark.parametrize("Sq,H", [(1, 16), (2, 16), (3, 32), (1, 128)])
+@pytest.mark.parametrize("Sq,H", [(1, 16), (2, 16), (3, 32), (1, 128), (2, 64), (3, 128)])
 def test_window_mla_fp8(cuda_device, Sq, H, page, window, first, parts):
     check_window("mla_fp8", LENGTHS, Sq, H, 1, page, window, first, Sq > 1, seed=page + window, parts=parts)
 
@@ -225,7 +231,7 @@ def test_window_mha(cuda_device, Sq, H, Hkv, page, window, first):
         check_window("mha", LENGTHS, Sq, H, Hkv, page, window, first, Sq == 1, seed=H + page, parts=parts)
 
 
-@pytest.mark.parametrize("kind,H,Hkv", [("mla", 16, 1), ("mla", 128, 1), ("mla_fp8", 16, 1), ("mha", 32, 8)])
+@pytest.mark.parametrize("kind,H,Hkv", [("mla", 16, 1), ("mla", 128, 1), ("mla_fp8", 16, 1), ("mla_fp8", 128, 1), ("mha", 32, 8)])
 def test_long_window(cuda_device, kind, H, Hkv):
     """Lengths far past the window, a strided block table, a scale other than the usual one, negative and zero."""
     lengths = [30000, 12345, 4096, 4097, 9000, 1]
@@ -237,7 +243,7 @@ def test_long_window(cuda_device, kind, H, Hkv):
 def test_many_short_sequences(cuda_device):
     g = torch.Generator().manual_seed(3)
     lengths = torch.randint(0, 200, (700,), generator=g).tolist()
-    for kind, H, Hkv in (("mla", 16, 1), ("mla", 128, 1), ("mla_fp8", 16, 1), ("mha", 8, 2)):
+    for kind, H, Hkv in (("mla", 16, 1), ("mla", 128, 1), ("mla_fp8", 16, 1), ("mla_fp8", 128, 1), ("mha", 8, 2)):
         check_window(kind, lengths, 1, H, Hkv, 32, 50, 3, False, seed=4)
 
 
@@ -263,7 +269,7 @@ def test_large_cache_offsets(cuda_device):
         close(out, lse, reference(q, [(k[:, None], k[:, None, :512])], [seen_mask(L, 1, 0, 0)], 576 ** -0.5, None, 512))
 
 
-@pytest.mark.parametrize("kind,H,Hkv", [("mla", 16, 1), ("mla", 128, 1), ("mla_fp8", 16, 1), ("mha", 32, 8)])
+@pytest.mark.parametrize("kind,H,Hkv", [("mla", 16, 1), ("mla", 128, 1), ("mla_fp8", 16, 1), ("mla_fp8", 128, 1), ("mha", 32, 8)])
 def test_same_result_again_on_a_stream_and_in_a_graph(cuda_device, kind, H, Hkv):
     run, ref, (out, lse), (plan, ws, *_) = make_window(kind, [5, 900, 0, 333, 2000], 1, H, Hkv, 16, 300, 4, True, seed=9)
     run(out, lse)
@@ -289,7 +295,7 @@ def test_same_result_again_on_a_stream_and_in_a_graph(cuda_device, kind, H, Hkv)
 
 def test_bad_pages_and_lengths_are_flagged(cuda_device):
     """An entry outside the cache reads as zeros and is reported; a length past L_max is clamped and reported."""
-    for kind, H, Hkv in (("mla", 16, 1), ("mla", 128, 1), ("mla_fp8", 32, 1), ("mha", 8, 2)):
+    for kind, H, Hkv in (("mla", 16, 1), ("mla", 128, 1), ("mla_fp8", 32, 1), ("mla_fp8", 128, 1), ("mha", 8, 2)):
         run, ref, (out, lse), (plan, ws, pages, sl, q) = make_window(kind, [100, 300, 260], 1, H, Hkv, 64, 0, 0, False, 11)
         for bad in (-1, pages.num, 2 ** 31 - 1, -2 ** 31):
             good = int(pages.table[1, 2])
@@ -590,12 +596,12 @@ def test_append_many_sequences_and_no_tokens(cuda_device):
 
 # ---------------------------------------------------------------- together
 
-@pytest.mark.parametrize("fp8,H", [(False, 16), (False, 128), (True, 16)])
-def test_append_then_decode(cuda_device, fp8, H):
+@pytest.mark.parametrize("fp8,H,page", [(False, 16, 16), (False, 128, 16), (True, 16, 16), (True, 128, 32)])
+def test_append_then_decode(cuda_device, fp8, H, page):
     """Three steps of a server: prompts of odd lengths are appended, then tokens one by one, and each step's decode
     equals the 64-bit one over all that was appended; the whole step is captured once and replayed."""
     g = torch.Generator(device=DEV).manual_seed(2)
-    prompts, page, window, first = [37, 1, 200, 90], 16, 64, 4
+    prompts, window, first = [37, 1, 200, 90], 64, 4
     B, total = 4, [n + 3 for n in prompts]
     pages = Pages("mla_fp8" if fp8 else "mla", total, page, seed=3)
     cos_sin = M.rope_table(400, 64, device=DEV)
