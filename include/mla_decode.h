@@ -442,9 +442,8 @@ mla_status mla_decode_run_fp8_phase(const mla_plan* plan, const void* q, const v
  *                 other sizes in [1, 2^24]); multiples of 64 load fastest
  *   window        >= 0, 0 = none;  first_tokens  in [0, 2^24], used with a window
  * mha_decode_plan_paged -- as mha_decode_plan, with the same three.
- * mla_decode_plan_paged_fp8 -- the same for pages of E4M3 codes; the plan's kernel
- * is MLA_KERNEL_FP8_PAIR when Sq*H is a multiple of 128 and page_size one of 32,
- * else MLA_KERNEL_FP8_MMA.  (Both hold lse to the precision of their scores: they
+ * mla_decode_plan_paged_fp8 -- the same for pages of E4M3 codes, with the kernels
+ * of mla_decode_plan_fp8.  (Both hold lse to the precision of their scores: they
  * sum the weights before their rounding.)
  */
 mla_status mla_decode_plan_paged(int32_t B, int32_t Sq, int32_t H, int32_t L_max, int32_t page_size, int32_t window,

@@ -30,8 +30,8 @@
 // the leader's QK^T issuer waits until both CTAs have written theirs.
 //
 // In pages (CV = PagedKv): as in kernel_pair.cuh, a V slot being [128 / box][2
-// chunks][box rows][64 bytes]; the PV steps take 32 keys, so a box has at least
-// 32 rows.
+// chunks][box rows][64 bytes].  The PV steps take 32 keys, which boxes of 16
+// rows would split; those are loaded a chunk at a time, as [2 chunks][128 rows].
 #pragma once
 
 #include <cuda.h>
@@ -245,7 +245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     const uint32_t lead_q_full = ptx::mapa_shared(ptx::smem_u32(q_full), 0);
     const bool stall_cta = (blockIdx.x == 0);
     uint32_t box_rows = kTileKV;
-    if constexpr (CV::kPaged) box_rows = static_cast<uint32_t>(pa.box);
+    if constexpr (CV::kPaged) box_rows = pa.box >= 32 ? pa.box : kTileKV;  // rows of a V box as it lies in its slot
 
     if (warp == 4) {
         // ============================================================ K producer
@@ -253,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             uint32_t k_cnt = 0;
             int unit = 1;  // (as below, but a later piece's Q has no number)
             // the boxes of this CTA's 64 rows of a tile
-            BoxList<Walker, 2> boxes(pa, walker, smem + C::OFF_LIST, lane, static_cast<int>(rank) * 64, 6);
+            BoxList<Walker, 4> boxes(pa, walker, smem + C::OFF_LIST, lane, static_cast<int>(rank) * 64, 6);
             const uint32_t box_bytes = static_cast<uint32_t>(kChunk) << pa.box_log2;
             const bool ok = boxes.run(args.status, [&](int tile, bool more) -> bool {
                 if (more && args.prefetch_tiles > 0)  // the next tile into L2, K and V columns alike
@@ -365,8 +365,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         // ============================================================ V producer
         if constexpr (CV::kPaged) {
             uint32_t v_cnt = 0;
-            BoxList<Walker, 4> boxes(pa, walker, smem + C::OFF_LIST + 512, lane, 0, 7);
-            const uint32_t box_bytes = 2u * kChunk << pa.box_log2;  // two chunks
+            BoxList<Walker, 8> boxes(pa, walker, smem + C::OFF_LIST + 512, lane, 0, 7);
+            const bool by_chunk = pa.box < 32;
+            const uint32_t box_bytes = (by_chunk ? 1u : 2u) * kChunk << pa.box_log2;
             const bool ok = boxes.run(args.status, [&](int tile, bool) -> bool {
                 const auto box = boxes.get(tile);
 #pragma unroll 1
@@ -375,10 +376,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                     if (!ptx::mbar_wait_bounded(v_empty + s, ((v_cnt / NV) & 1) ^ 1, tmo)) return false;
                     if (leader) ptx::mbar_arrive_expect_tx(v_full + s, 2 * C::kVSlot);
                     const int col0 = 256 * i + 128 * static_cast<int>(rank);  // two adjacent chunks, one box
+                    const uint32_t full = ptx::mapa_shared(ptx::smem_u32(v_full + s), 0);
                     box.each([&](int k, int row, int page) {
-                        ptx::tma_load_4d_pair(v_smem + s * C::kVSlot + k * box_bytes, &tm_v,
-                                              ptx::mapa_shared(ptx::smem_u32(v_full + s), 0), 0, row, col0 / kChunk,
-                                              page);
+                        uint8_t* dst = v_smem + s * C::kVSlot + k * box_bytes;
+                        if (by_chunk) {
+                            ptx::tma_load_3d_pair(dst, &tm_k, full, col0, row, page);
+                            ptx::tma_load_3d_pair(dst + C::kVChunk, &tm_k, full, col0 + kChunk, row, page);
+                        } else {
+                            ptx::tma_load_4d_pair(dst, &tm_v, full, 0, row, col0 / kChunk, page);
+                        }
                     });
                     ++v_cnt;
                 }

@@ -276,11 +276,7 @@ mla_status mla_decode_plan_paged_fp8(int32_t B, int32_t Sq, int32_t H, int32_t L
                                      int32_t num_partitions_override, mla_plan* plan, size_t* workspace_bytes) {
     if (!plan) return MLA_ERR_INVALID_ARG;
     mla_plan p;
-    // the CTA-pair kernel as for a contiguous cache, where a page divides into
-    // boxes of 32 rows; the transposed operand kernel takes any
-    const int32_t kernel = page_size % 32 == 0 ? 0 : MLA_KERNEL_FP8_MMA;
-    mla_status st =
-        mla_decode_plan_fp8_kernel(B, Sq, H, L_max, device, num_partitions_override, kernel, &p, nullptr);
+    mla_status st = mla_decode_plan_fp8_kernel(B, Sq, H, L_max, device, num_partitions_override, 0, &p, nullptr);
     if (st == MLA_OK) st = check_page_args(page_size, window, first_tokens);
     if (st != MLA_OK) return st;
     if (p.kernel == MLA_KERNEL_FP8_PAIR) p.smem_bytes = PairFp8PagedC::kSmemBytes;
@@ -303,7 +299,7 @@ mla_status mla_decode_run_paged_fp8(const mla_plan* plan, const void* q, const v
     const mla_plan& pl = *plan;
     const int R = pl.Sq * pl.H, G = pl.group_rows;
     const bool pair = pl.kernel == MLA_KERNEL_FP8_PAIR;
-    if (!(pair ? G == 128 && pl.page_size % 32 == 0 : pl.kernel == MLA_KERNEL_FP8_MMA && (G == 16 || G == 32)) ||
+    if (!(pair ? G == 128 : pl.kernel == MLA_KERNEL_FP8_MMA && (G == 16 || G == 32)) ||
         pl.Hkv != 1 || pl.head_dim != mla::kDqk || G * pl.num_groups != R || pl.prefix_max != 0 ||
         !(std::isfinite(kv_scale) && kv_scale > 0.f))
         return MLA_ERR_INVALID_ARG;

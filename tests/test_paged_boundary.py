@@ -24,8 +24,7 @@ def test_plans():
     assert (p.kernel, p.page_size, p.window, p.first_tokens) == (M.MLA_KERNEL_PAIR, 64, 1000, 4)
     assert p.workspace_bytes == M.mla_decode_plan(4, 1, 128, 5000, device=-1).workspace_bytes
     assert M.mla_decode_plan_paged(4, 1, 16, 5000, 16, device=-1).kernel == M.MLA_KERNEL_TRANSPOSED
-    assert M.mla_decode_plan_paged_fp8(4, 1, 128, 5000, 16, device=-1).kernel == M.MLA_KERNEL_FP8_MMA
-    assert M.mla_decode_plan_paged_fp8(4, 1, 128, 5000, 96, device=-1).kernel == M.MLA_KERNEL_FP8_PAIR
+    assert M.mla_decode_plan_paged_fp8(4, 1, 128, 5000, 16, device=-1).kernel == M.MLA_KERNEL_FP8_PAIR
     assert M.mla_decode_plan_paged_fp8(4, 1, 16, 5000, 64, device=-1).kernel == M.MLA_KERNEL_FP8_MMA
     assert M.mha_decode_plan_paged(4, 1, 32, 8, 5000, 16, device=-1).kernel == M.MLA_KERNEL_MHA
     # few heads and much to read: a launch of its own for the prefix, 160 rows in two groups of 128
