@@ -118,14 +118,15 @@ __device__ __forceinline__ uint64_t bits_between(int lo, int hi) {
     return lo >= 64 ? 0ull : lo <= 0 ? below : below & ~((1ull << lo) - 1);
 }
 
-// Row i of a sequence is seen by none of its tokens.
+// Rows to clear: those that no token sees in boxes that were loaded.  (Boxes past
+// the sequence's end are zeros as TMA wrote them.)
 __device__ __forceinline__ bool unseen(const PagedArgs& a, const SeqView& v, int i) {
-    return i >= v.rows || (i < v.lo && i >= v.f);
+    return (i >= v.rows && i < ((v.rows + a.box - 1) & -a.box)) || (i < v.lo && i >= v.f);
 }
-// Some row of tile t is seen by none: the tile's values are cleared there.
+// Tile t has such rows.
 __device__ __forceinline__ bool tile_unseen(const PagedArgs& a, const SeqView& v, int t) {
     const int i = t * kTileKV;
-    return i + kTileKV > v.rows || (i < v.lo && i + kTileKV > v.f);
+    return (i + kTileKV > v.rows && (v.rows & (a.box - 1))) || (i < v.lo && i + kTileKV > v.f);
 }
 
 // The boxes of a partition's tiles, found by a producer warp for the one of its
