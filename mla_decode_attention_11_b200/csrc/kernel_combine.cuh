@@ -59,11 +59,16 @@ inline int combine_grid_y(int B, int R, int num_sms) {
 // DV: value width (512 for MLA, 128 for MHA); a lane owns DV / 128 float4 columns.
 // CV: where the lengths come from (paged.cuh); in a paged run a row may have
 // seen no key of any piece: it gets out = 0 and lse = -inf (or its sink).
-template <int DV = kDv, class CV = ContigKv>
+// kNarrow: a warp takes 128 columns of a row with 16 partials in flight, instead
+// of the whole row with 4: for few rows of many pieces, where rows alone leave
+// warps without work.
+template <int DV = kDv, class CV = ContigKv, bool kNarrow = false>
 __global__ void __launch_bounds__(kCombineThreads, 2)
     mla_decode_combine_kernel(const CombineArgs args, const __grid_constant__ typename CV::Args pa) {
     static_assert(DV == 512 || DV == 128, "value width");
-    constexpr int NV4 = DV / 128;  // float4 columns per lane
+    constexpr int NC = kNarrow ? DV / 128 : 1;  // column groups of a row
+    constexpr int NV4 = DV / 128 / NC;          // float4 columns per lane
+    constexpr int KB = kNarrow ? 16 : 4;        // partials in flight
     __shared__ int s_split;
     __shared__ long long s_acc, s_tot;
     const int b = blockIdx.x;
@@ -86,13 +91,17 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
     ptx::wait_prior_grid();
     const int S = s_split;
     const long long acc = s_acc, tot = s_tot;
-    const int rows_per = (args.R + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
-    const int r_lo = static_cast<int>(blockIdx.y) * rows_per;
-    const int r_hi = r_lo + rows_per < args.R ? r_lo + rows_per : args.R;
+    // this CTA's (row, column group) units
+    const int units = args.R * NC;
+    const int units_per = (units + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
+    const int u_lo = static_cast<int>(blockIdx.y) * units_per;
+    const int u_hi = u_lo + units_per < units ? u_lo + units_per : units;
     const int L = make_lens(args, pa)(b);
     const long long n = num_units(L, S);
     if (n == 0) {
-        for (int r = r_lo + warp; r < r_hi; r += kCombineWarps) {
+        for (int u = u_lo + warp; u < u_hi; u += kCombineWarps) {
+            if (NC > 1 && u % NC != 0) continue;
+            const int r = u / NC;
             const size_t orow = static_cast<size_t>(b) * args.R + r;
             // a per-head sink is one more softmax term without a value (-inf: none)
             const float sink = args.sinks ? args.sinks[r % args.H] : -INFINITY;
@@ -121,20 +130,21 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
         return (i == 0) ? 2 * p0 + 1 : 2 * (p0 + i);
     };
 
-    for (int r = r_lo + warp; r < r_hi; r += kCombineWarps) {
+    for (int u = u_lo + warp; u < u_hi; u += kCombineWarps) {
+        const int r = u / NC, col = (u % NC) * 32 + lane;  // first float4 column of the lane
         const size_t orow = static_cast<size_t>(b) * args.R + r;
         const float sink = args.sinks ? args.sinks[r % args.H] : -INFINITY;
         auto prow_of = [&](int i) { return static_cast<size_t>(slot_of(i)) * args.R + r; };
-        // the first (up to) 4 partial rows are requested before the lse values
-        // are reduced, so a row cut into at most 4 pieces costs one round trip
-        float4 x[4][NV4];
+        // the first (up to) KB partial rows are requested before the lse values
+        // are reduced, so a row cut into at most KB pieces costs one round trip
+        float4 x[KB][NV4];
         auto load_batch = [&](int i0) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < KB; ++j) {
                 if (i0 + j < k) {
                     const float4* src = reinterpret_cast<const float4*>(args.part_o + prow_of(i0 + j) * DV);
 #pragma unroll
-                    for (int v = 0; v < NV4; ++v) x[j][v] = __ldcs(src + lane + 32 * v);
+                    for (int v = 0; v < NV4; ++v) x[j][v] = __ldcs(src + col + 32 * v);
                 }
             }
         };
@@ -157,14 +167,14 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
         const float inv = (CV::kPaged && sum == 0.f) ? 0.f : 1.f / sum;
         const float my_w = my_e * inv;  // weight of piece `lane`: exp(lse_lane - lse)
 
-        // out = sum_i exp(lse_i - lse) * (O_i / l_i); lane owns float4 columns lane + 32 v
+        // out = sum_i exp(lse_i - lse) * (O_i / l_i); lane owns float4 columns col + 32 v
         float4 acc_o[NV4];
 #pragma unroll
         for (int v = 0; v < NV4; ++v) acc_o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = 0; i0 < k; i0 += 4) {
+        for (int i0 = 0; i0 < k; i0 += KB) {
             if (i0 > 0) load_batch(i0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < KB; ++j) {
                 const int i = i0 + j;
                 if (i < k) {
                     const float w = i < 32 ? __shfl_sync(0xffffffffu, my_w, i)
@@ -182,7 +192,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
         __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(args.out + orow * DV);
 #pragma unroll
         for (int v = 0; v < NV4; ++v) {
-            const int e0 = (lane + 32 * v) * 4;  // first column of acc_o[v]
+            const int e0 = (col + 32 * v) * 4;  // first column of acc_o[v]
             const __nv_bfloat162 lo = __floats2bfloat162_rn(acc_o[v].x, acc_o[v].y);
             const __nv_bfloat162 hi = __floats2bfloat162_rn(acc_o[v].z, acc_o[v].w);
             uint2 pk;
@@ -190,7 +200,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
             pk.y = *reinterpret_cast<const uint32_t*>(&hi);
             *reinterpret_cast<uint2*>(dst + e0 / 2) = pk;
         }
-        if (lane == 0) args.lse[orow] = lse_all;
+        if (lane == 0 && (NC == 1 || col == 0)) args.lse[orow] = lse_all;
     }
 }
 
