@@ -318,6 +318,32 @@ def test_bad_pages_and_lengths_are_flagged(cuda_device):
         close(out, lse, ref)
 
 
+@pytest.mark.parametrize("kind,H,Hkv", [("mla", 16, 1), ("mla", 128, 1), ("mla_fp8", 16, 1), ("mla_fp8", 128, 1), ("mha", 8, 2)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 300, 299])
+def test_windows_around_the_longest_length(cuda_device, kind, H, Hkv, window):
+    check_window(kind, [300, 299, 1, 0, 128], 2, H, Hkv, 32, window, 3, False, 13)
+
+
+# unit 2 is the last that CTA 0 loads of a single tile of grouped kv heads (0: queries, 1: keys, 2: values)
+@pytest.mark.parametrize("unit,parts", [(2, 0), (30, 1)])
+@pytest.mark.parametrize("kind,H,Hkv", [("mla", 16, 1), ("mla", 128, 1), ("mla_fp8", 16, 1), ("mla_fp8", 128, 1), ("mha", 8, 2)])
+def test_bounded_wait_timeout_reports_and_recovers(cuda_device, kind, H, Hkv, unit, parts):
+    """The producer of CTA 0 arms a barrier and leaves out its load: the consumers' waits run out after 20 ms, every
+    role unwinds, the run reports MLA_ERR_TIMEOUT and the next one on the same workspace is clean."""
+    run, ref, (out, lse), (plan, ws, *_) = make_window(kind, [1000, 990], 1, H, Hkv, 64, 0, 0, False, 17, parts=parts)
+    try:
+        M.mla_decode_set_debug(wait_timeout_ns=20_000_000, stall_unit=unit)
+        run(out, lse)
+        with pytest.raises(M.MlaError) as e:
+            M.mla_decode_check(plan, ws)
+        assert e.value.code == 5
+    finally:
+        M.mla_decode_set_debug(0, -1)
+    run(out, lse)
+    M.mla_decode_check(plan, ws)
+    close(out, lse, ref)
+
+
 # ---------------------------------------------------------------- shared prefix
 
 def make_prefix(lengths, Sq, H, P, page, sinks, seed, parts=0, prefix_max=None, L_max=None):
@@ -349,6 +375,7 @@ def make_prefix(lengths, Sq, H, P, page, sinks, seed, parts=0, prefix_max=None, 
 
     def run(out, lse):
         M.mla_decode_run_prefix(plan, q, pages.k, prefix_table, pl, pages.table[:B], sl, scale, out, lse, ws, sinks=sk)
+    run.q = q
     return run, ref, blank(B, Sq, H, 512), (plan, ws, pages, sl, pl)
 
 
@@ -644,14 +671,23 @@ def test_append_then_decode(cuda_device, fp8, H, page):
               f"step {i}")
 
 
-def test_prefix_equals_whole_sequences(cuda_device):
-    """The shared-prefix decode of a batch is the plain paged decode of the same sequences with the prefix's pages in
-    front of their own."""
-    P, page, H, lengths = 256, 64, 128, [1, 100, 64]
-    run, ref, (out, lse), (plan, ws, pages, sl, pl) = make_prefix(lengths, 1, H, P, page, False, seed=8)
+@pytest.mark.parametrize("most", [0, LONG])
+@pytest.mark.parametrize("H", [16, 128])
+def test_prefix_equals_whole_sequences(cuda_device, H, most):
+    """The shared-prefix decode of a batch against the plain paged decode of the same sequences with the prefix's pages
+    in front of their own: both are within their tolerances of the same values, so within twice them of each other."""
+    P, page, lengths = 256, 64, [1, 100, 64]
+    run, ref, (out, lse), (plan, ws, pages, sl, pl) = make_prefix(lengths, 1, H, P, page, False, seed=8, prefix_max=most)
     run(out, lse)
     M.mla_decode_check(plan, ws)
     close(out, lse, ref)
+    table = torch.cat([pages.table[3, :P // page].expand(3, -1), pages.table[:3, :2]], 1).contiguous()
+    whole = M.mla_decode_plan_paged(3, 1, H, P + 128, page, device=0)
+    ws = M.alloc_workspace(whole)
+    out2, lse2 = blank(3, 1, H, 512)
+    M.mla_decode_run_paged(whole, run.q, pages.k, table, sl + P, 576 ** -0.5, out2, lse2, ws)
+    M.mla_decode_check(whole, ws)
+    close(out2, lse2, ref)
 
 
 def test_refusals(cuda_device):
