@@ -53,6 +53,7 @@ struct AppendArgs {
     void* k_pages;              // MLA: the cache's rows of 576
     __nv_bfloat16* v_pages;
     float kv_scale;             // E4M3 cache
+    float kv_inv;               // 1 / kv_scale rounded, or 0 where that or its products could leave fp32's range
 };
 
 constexpr int kAppendThreads = 128;
@@ -130,12 +131,22 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// x / scale from the reciprocal inv: the product and one correction by its exact
+// remainder, which gives the correctly rounded quotient (Markstein, IBM J. Res.
+// Dev. 34, 1990).  A division of each of 576 columns took 2 of 12.7 us for 8168
+// tokens.  Beyond what E4M3 holds the product itself will do (infinities, NaN).
+__device__ __forceinline__ float quotient(float x, float scale, float inv) {
+    const float q = x * inv;
+    return fabsf(q) < 1024.f ? fmaf(fmaf(-q, scale, x), inv, q) : q;
+}
+
 // Eight E4M3 codes of x / scale, saturated at +-448 (round to nearest even).
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale) {
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale, float inv) {
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 y = make_float2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale));
+        const float2 y = inv != 0.f ? make_float2(quotient(x[2 * i], scale, inv), quotient(x[2 * i + 1], scale, inv))
+                                    : make_float2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale));
         const uint32_t c = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
         w[i >> 1] |= (c & 0xFFFFu) << (16 * (i & 1));
     }
@@ -270,9 +281,9 @@ __global__ void __launch_bounds__(kAppendThreads) mla_cache_append_kernel(const 
         float y[8], z[8];
         unpack8(r0, y);
         unpack8(r1, z);
-        const uint2 lo = quantise8(y, a.kv_scale), hi = quantise8(z, a.kv_scale);
+        const uint2 lo = quantise8(y, a.kv_scale, a.kv_inv), hi = quantise8(z, a.kv_scale, a.kv_inv);
         *reinterpret_cast<uint4*>(dst + c0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-        if (lane < 8) *reinterpret_cast<uint2*>(dst + kDv + col) = quantise8(x, a.kv_scale);
+        if (lane < 8) *reinterpret_cast<uint2*>(dst + kDv + col) = quantise8(x, a.kv_scale, a.kv_inv);
     } else {
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.k_pages) + row * kDqk;
         *reinterpret_cast<uint4*>(dst + c0) = r0;

@@ -588,6 +588,8 @@ mla_status append_args(const mla_append* p, bool mha, mla::AppendArgs& a) {
     a.k_pages = p->k_pages;
     a.v_pages = static_cast<__nv_bfloat16*>(p->v_pages);
     a.kv_scale = p->kv_scale;
+    // (of bf16 values: at most 2^128, at least 2^-133)
+    a.kv_inv = p->kv_scale > 0x1p-100f && p->kv_scale < 0x1p100f ? 1.f / p->kv_scale : 0.f;
     return MLA_OK;
 }
 

@@ -555,6 +555,23 @@ def test_append_mha(cuda_device, H, Hkv, page, rot, interleaved):
             assert ((q_out.double() - want).abs() <= turn_tolerance(keep[:, :H], rot)(want)).all()
 
 
+@pytest.mark.parametrize("scale", [1 / 60, 1.0, 3.0, 0.0123, 2.0 ** -110, 2.0 ** 110, 1e-30, 7e29])
+def test_append_quantises_every_value(cuda_device, scale):
+    """Every finite bf16 value of the latent columns, and infinities and NaN, against a division in 32 bits."""
+    bits = torch.arange(65536, device=DEV).to(torch.int32).to(torch.int16)
+    x = bits.view(torch.bfloat16).view(128, 512)
+    kv = torch.zeros(8, 16, 576, dtype=torch.uint8, device=DEV)
+    rope = torch.zeros(128, 64, dtype=torch.bfloat16, device=DEV)
+    table = torch.arange(8, dtype=torch.int32, device=DEV)[None]
+    sl = torch.tensor([128], dtype=torch.int32, device=DEV)
+    M.mla_cache_append(x, rope, M.rope_table(128, 64, device=DEV), kv, table, sl, kv_scale=scale)
+    got = kv.flatten(0, 1)[:, :512].contiguous().view(torch.float8_e4m3fn).float()
+    want = (x.float() / torch.tensor(scale, device=DEV)).clamp(-448, 448).to(torch.float8_e4m3fn).float()
+    nan = torch.isnan(x.float())
+    assert torch.isnan(got[nan]).all()
+    assert torch.equal(got[~nan], want[~nan])
+
+
 def test_append_uniform_padded_and_unplaced_tokens(cuda_device):
     """cu_tokens None: the same number for each; tokens past the last bound are padding; a token without a position or
     page is reported, and the others are written."""
