@@ -489,9 +489,8 @@ mla_status mha_decode_run_paged(const mla_plan* plan, const void* q, const void*
 /*
  * Shared prefix.  All sequences of the batch start with the same prefix_len
  * keys (a system prompt, one prompt sampled many times), held once in the
- * cache; the batch attends to them once, 128 query rows of any sequences at a
- * time, instead of once per sequence.  seqlens[b] counts the sequence's own
- * keys, which follow the prefix and are in block_table:
+ * cache.  seqlens[b] counts the sequence's own keys, which follow the prefix and
+ * are in block_table:
  *     every query token sees every prefix key;
  *     token t sees the own keys j <= seqlens[b] - Sq + t.
  * The result is the softmax over both.  A sequence without own keys
@@ -499,8 +498,12 @@ mla_status mha_decode_run_paged(const mla_plan* plan, const void* q, const void*
  *
  * mla_decode_plan_prefix -- as mla_decode_plan_paged without a window:
  *   L_max       most own keys of a sequence;  prefix_max  most prefix keys (1..2^24)
- * The workspace holds one fp32 partial per query row for the prefix and one
- * for its own keys, besides those of cut pieces.
+ * The products with the prefix are computed for 128 query rows at a time: where
+ * Sq * H is a multiple of 128, a sequence's own rows, in one launch with its own
+ * keys; else rows of any sequences, in a launch of its own (prefix_partitions > 0;
+ * the workspace then holds one fp32 partial per query row for the prefix and one
+ * for its own keys, besides those of cut pieces) -- unless prefix_max is so short
+ * that reading it once per sequence is quicker.
  *
  * mla_decode_run_prefix -- enqueue one such decode.
  *   prefix_table  device, int32, the prefix's pages in order, prefix_width
