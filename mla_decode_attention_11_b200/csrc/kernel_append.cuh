@@ -12,11 +12,12 @@
 // multiply-add, so the result is the one elementary operations give).
 //
 // Bound by HBM: every input is read once and every output written once, and a
-// token needs only its own rows.  A warp takes one task -- a token's cache row,
-// or 8 (128 wide) / 16 (64 wide) head rows of it, about 2 KB -- with all of its
-// 16-byte loads issued before the position is known, so the dependent chain
-// (which sequence, its length, its angles) overlaps them; a prefill has some
-// 10^4 tasks, enough to cover the latency with occupancy alone.
+// token needs only its own rows.  Its work is in tasks of about 2 KB -- its cache
+// row, or 8 (128 wide) / 16 (64 wide) head rows -- dealt to `parts` warps: one
+// where there are tokens enough to fill the GPU (which sequence, its length, its
+// page and its angles, a chain of loads, are then found once), more where there
+// are few.  A warp issues its first task's loads before it looks for the token's
+// place, and each further task's before it writes the one at hand.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -209,10 +210,8 @@ struct HeadRows {
         }
     }
     template <bool kInterleaved>
-    __device__ __forceinline__ void turn(const float* angles, int rot, int lane) {
+    __device__ __forceinline__ void turn(const Angles<kInterleaved>& ang, int rot, int lane) {
         const int col = (lane % kLanes) * 8;
-        Angles<kInterleaved> ang;
-        if (col < rot) ang.load(angles, col, rot);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             float x[8];
@@ -230,99 +229,131 @@ struct HeadRows {
     }
 };
 
-template <int W, bool kInterleaved>
-__device__ __forceinline__ void query_task(const AppendArgs& a, int i, int chunk, int lane) {
-    using R = HeadRows<W>;
-    const int h0 = chunk * R::kHeads;
-    const int n = a.H - h0 < R::kHeads ? a.H - h0 : R::kHeads;
-    R rows;
-    rows.load(a.q_in + i * a.qi_token + h0 * a.qi_head, a.qi_head, n, lane);
-    int b, pos;
-    place_token(a, i, lane, b, pos);
-    if (pos < 0) return;
-    rows.template turn<kInterleaved>(a.cos_sin + static_cast<long long>(pos) * a.rot, a.rot, lane);
-    rows.store(a.q_out + i * a.qo_token + h0 * a.qo_head, a.qo_head, n, lane);
+// The token and part of this warp: grid (T / warps a block, parts).
+__device__ __forceinline__ long long token_of_warp() {
+    return static_cast<long long>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);
 }
 
-// Latent cache: task 0 of a token is its row [latent 512 | turned k_rope 64],
-// the others 16 of its query heads' rope columns.
+// Latent cache: a token's task 0 is its row [latent 512 | turned k_rope 64], the
+// others 16 of its query heads' rope columns each.
 template <bool kFp8, bool kInterleaved>
-__global__ void __launch_bounds__(kAppendThreads) mla_cache_append_kernel(const AppendArgs a, int tasks_per_token) {
-    const int lane = threadIdx.x & 31;
-    const long long w = (static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x) >> 5;
-    const long long token = w / tasks_per_token;
+__global__ void __launch_bounds__(kAppendThreads) mla_cache_append_kernel(const AppendArgs a) {
+    using R = HeadRows<64>;
+    const int lane = threadIdx.x & 31, parts = gridDim.y;
+    const long long token = token_of_warp();
     if (token >= a.T) return;
     const int i = static_cast<int>(token);
-    const int task = static_cast<int>(w - token * tasks_per_token);
-    if (task > 0) {
-        query_task<64, kInterleaved>(a, i, task - 1, lane);
-        return;
-    }
+    const int tasks = 1 + (a.H + R::kHeads - 1) / R::kHeads;
+    const bool row_here = blockIdx.y == 0;
+    int task = row_here ? parts : blockIdx.y;  // the first task of heads
+    const __nv_bfloat16* q_in = a.q_in + i * a.qi_token;
+    auto heads = [&](int t) { return a.H - (t - 1) * R::kHeads < R::kHeads ? a.H - (t - 1) * R::kHeads : R::kHeads; };
+    auto load = [&](R& rows, int t) { rows.load(q_in + (t - 1) * R::kHeads * a.qi_head, a.qi_head, heads(t), lane); };
+    R rows;
+    if (task < tasks) load(rows, task);
     const __nv_bfloat16* latent = a.k + i * a.k_token;
     // bf16: columns 8 lane, 256 + 8 lane (rows of 512 bytes a step); E4M3: 16 lane .. 16 lane + 15 (16 bytes of codes)
     const int c0 = kFp8 ? 16 * lane : 8 * lane, c1 = kFp8 ? 16 * lane + 8 : 256 + 8 * lane;
-    const uint4 r0 = *reinterpret_cast<const uint4*>(latent + c0);
-    const uint4 r1 = *reinterpret_cast<const uint4*>(latent + c1);
-    float x[8];
     const int col = (lane & 7) * 8;
-    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if (lane < 8) raw = *reinterpret_cast<const uint4*>(a.v + i * a.v_token + col);
+    uint4 r0, r1, raw = make_uint4(0u, 0u, 0u, 0u);
+    if (row_here) {
+        r0 = *reinterpret_cast<const uint4*>(latent + c0);
+        r1 = *reinterpret_cast<const uint4*>(latent + c1);
+        if (lane < 8) raw = *reinterpret_cast<const uint4*>(a.v + i * a.v_token + col);
+    }
     int b, pos;
     place_token(a, i, lane, b, pos);
     if (pos < 0) return;
-    const long long row = cache_row(a, b, pos, lane);
-    if (row < 0) return;
     Angles<kInterleaved> ang;
     ang.load(a.cos_sin + static_cast<long long>(pos) * a.rot, col, a.rot);
-    unpack8(raw, x);
-    turn8<kInterleaved>(x, ang, col, a.rot, lane);
-    if constexpr (kFp8) {
-        uint8_t* dst = static_cast<uint8_t*>(a.k_pages) + row * kDqk;
-        float y[8], z[8];
-        unpack8(r0, y);
-        unpack8(r1, z);
-        const uint2 lo = quantise8(y, a.kv_scale, a.kv_inv), hi = quantise8(z, a.kv_scale, a.kv_inv);
-        *reinterpret_cast<uint4*>(dst + c0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-        if (lane < 8) *reinterpret_cast<uint2*>(dst + kDv + col) = quantise8(x, a.kv_scale, a.kv_inv);
-    } else {
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.k_pages) + row * kDqk;
-        *reinterpret_cast<uint4*>(dst + c0) = r0;
-        *reinterpret_cast<uint4*>(dst + c1) = r1;
-        if (lane < 8) *reinterpret_cast<uint4*>(dst + kDv + col) = pack8(x);
+    const long long row = row_here ? cache_row(a, b, pos, lane) : -1;
+    if (row >= 0) {
+        float x[8];
+        unpack8(raw, x);
+        turn8<kInterleaved>(x, ang, col, a.rot, lane);
+        if constexpr (kFp8) {
+            uint8_t* dst = static_cast<uint8_t*>(a.k_pages) + row * kDqk;
+            float y[8], z[8];
+            unpack8(r0, y);
+            unpack8(r1, z);
+            const uint2 lo = quantise8(y, a.kv_scale, a.kv_inv), hi = quantise8(z, a.kv_scale, a.kv_inv);
+            *reinterpret_cast<uint4*>(dst + c0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            if (lane < 8) *reinterpret_cast<uint2*>(dst + kDv + col) = quantise8(x, a.kv_scale, a.kv_inv);
+        } else {
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.k_pages) + row * kDqk;
+            *reinterpret_cast<uint4*>(dst + c0) = r0;
+            *reinterpret_cast<uint4*>(dst + c1) = r1;
+            if (lane < 8) *reinterpret_cast<uint4*>(dst + kDv + col) = pack8(x);
+        }
+    }
+    __nv_bfloat16* q_out = a.q_out + i * a.qo_token;
+    for (; task < tasks; task += parts) {
+        R next;
+        if (task + parts < tasks) load(next, task + parts);
+        rows.template turn<kInterleaved>(ang, a.rot, lane);
+        rows.store(q_out + (task - 1) * R::kHeads * a.qo_head, a.qo_head, heads(task), lane);
+        rows = next;
     }
 }
 
 // Keys and values of grouped kv heads, 128 wide: a token's tasks are its key
 // heads (turned), its value heads (copied) and its query heads, 8 at a time.
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kAppendThreads) mha_cache_append_kernel(const AppendArgs a, int tasks_per_token) {
+__global__ void __launch_bounds__(kAppendThreads) mha_cache_append_kernel(const AppendArgs a) {
     using R = HeadRows<128>;
-    const int lane = threadIdx.x & 31;
-    const long long w = (static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x) >> 5;
-    const long long token = w / tasks_per_token;
+    const int lane = threadIdx.x & 31, parts = gridDim.y;
+    const long long token = token_of_warp();
     if (token >= a.T) return;
     const int i = static_cast<int>(token);
-    int task = static_cast<int>(w - token * tasks_per_token);
     const int kv_tasks = (a.Hkv + R::kHeads - 1) / R::kHeads;
-    if (task >= 2 * kv_tasks) {
-        query_task<128, kInterleaved>(a, i, task - 2 * kv_tasks, lane);
-        return;
-    }
-    const bool value = task >= kv_tasks;
-    if (value) task -= kv_tasks;
-    const int h0 = task * R::kHeads;
-    const int n = a.Hkv - h0 < R::kHeads ? a.Hkv - h0 : R::kHeads;
+    const int tasks = 2 * kv_tasks + (a.H + R::kHeads - 1) / R::kHeads;
+    struct Task {
+        int kind, h0, n;  // kind 0: keys, 1: values, 2: queries
+    };
+    auto task_at = [&](int t) {
+        Task k;
+        k.kind = t < kv_tasks ? 0 : t < 2 * kv_tasks ? 1 : 2;
+        k.h0 = (t - k.kind * kv_tasks) * R::kHeads;
+        const int heads = k.kind == 2 ? a.H : a.Hkv;
+        k.n = heads - k.h0 < R::kHeads ? heads - k.h0 : R::kHeads;
+        return k;
+    };
+    auto load = [&](R& rows, const Task& k) {
+        const __nv_bfloat16* from = k.kind == 0 ? a.k + i * a.k_token : k.kind == 1 ? a.v + i * a.v_token : a.q_in + i * a.qi_token;
+        const long long step = k.kind == 0 ? a.k_head : k.kind == 1 ? a.v_head : a.qi_head;
+        rows.load(from + k.h0 * step, step, k.n, lane);
+    };
+    int t = blockIdx.y;
+    Task at = task_at(t);
     R rows;
-    rows.load(value ? a.v + i * a.v_token + h0 * a.v_head : a.k + i * a.k_token + h0 * a.k_head,
-              value ? a.v_head : a.k_head, n, lane);
+    load(rows, at);
     int b, pos;
     place_token(a, i, lane, b, pos);
     if (pos < 0) return;
-    const long long row = cache_row(a, b, pos, lane);
-    if (row < 0) return;
-    if (!value) rows.template turn<kInterleaved>(a.cos_sin + static_cast<long long>(pos) * a.rot, a.rot, lane);
-    __nv_bfloat16* pages = value ? a.v_pages : static_cast<__nv_bfloat16*>(a.k_pages);
-    rows.store(pages + (row * a.Hkv + h0) * 128, 128, n, lane);
+    const int col = (lane % R::kLanes) * 8;
+    Angles<kInterleaved> ang;
+    if (col < a.rot) ang.load(a.cos_sin + static_cast<long long>(pos) * a.rot, col, a.rot);
+    const long long row = t < 2 * kv_tasks ? cache_row(a, b, pos, lane) : -1;
+    while (true) {
+        R next;
+        Task then;
+        const bool more = t + parts < tasks;
+        if (more) {
+            then = task_at(t + parts);
+            load(next, then);
+        }
+        if (at.kind != 1) rows.template turn<kInterleaved>(ang, a.rot, lane);
+        if (at.kind == 2) {
+            rows.store(a.q_out + i * a.qo_token + at.h0 * a.qo_head, a.qo_head, at.n, lane);
+        } else if (row >= 0) {
+            __nv_bfloat16* pages = at.kind == 1 ? a.v_pages : static_cast<__nv_bfloat16*>(a.k_pages);
+            rows.store(pages + (row * a.Hkv + at.h0) * 128, 128, at.n, lane);
+        }
+        if (!more) return;
+        t += parts;
+        at = then;
+        rows = next;
+    }
 }
 
 }  // namespace mla
