@@ -69,6 +69,11 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
     constexpr int NC = kNarrow ? DV / 128 : 1;  // column groups of a row
     constexpr int NV4 = DV / 128 / NC;          // float4 columns per lane
     constexpr int KB = kNarrow ? 16 : 4;        // partials in flight
+    // weights a lane keeps, one for every 32 pieces: 5 are those of as many pieces
+    // as a plan makes by itself (reading a weight again for each piece beyond the
+    // 32nd, one sequence of 78 pieces takes 27 instead of 22 us; where pieces are
+    // few, looking for them costs 0.3 us)
+    constexpr int kHeld = kNarrow ? 5 : 1;
     __shared__ int s_split;
     __shared__ long long s_acc, s_tot;
     const int b = blockIdx.x;
@@ -149,23 +154,33 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
             }
         };
         load_batch(0);
-        // merged lse: lane i holds piece i (pieces beyond 32 folded in by a loop)
-        const float my_l = lane < k ? args.part_lse[prow_of(lane)] : -INFINITY;
-        float m = my_l;
-        for (int i = lane + 32; i < k; i += 32) m = fmaxf(m, args.part_lse[prow_of(i)]);
+        // merged lse: lane i holds pieces i, i + 32, ... (those beyond 32 kHeld folded in by a loop)
+        float my_w[kHeld];
+        float m = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+            my_w[h] = lane + 32 * h < k ? args.part_lse[prow_of(lane + 32 * h)] : -INFINITY;
+            m = fmaxf(m, my_w[h]);
+        }
+        for (int i = lane + 32 * kHeld; i < k; i += 32) m = fmaxf(m, args.part_lse[prow_of(i)]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         m = fmaxf(m, sink);
         if (CV::kPaged && m == -INFINITY) m = 0.f;
-        const float my_e = lane < k ? expf(my_l - m) : 0.f;
-        float sum = my_e;
-        for (int i = lane + 32; i < k; i += 32) sum += expf(args.part_lse[prow_of(i)] - m);
+        float sum = 0.f;
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+            my_w[h] = lane + 32 * h < k ? expf(my_w[h] - m) : 0.f;
+            sum += my_w[h];
+        }
+        for (int i = lane + 32 * kHeld; i < k; i += 32) sum += expf(args.part_lse[prow_of(i)] - m);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         sum += expf(sink - m);
         const float lse_all = m + logf(sum);
         const float inv = (CV::kPaged && sum == 0.f) ? 0.f : 1.f / sum;
-        const float my_w = my_e * inv;  // weight of piece `lane`: exp(lse_lane - lse)
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) my_w[h] *= inv;  // weights of the lane's pieces: exp(lse_i - lse)
 
         // out = sum_i exp(lse_i - lse) * (O_i / l_i); lane owns float4 columns col + 32 v
         float4 acc_o[NV4];
@@ -173,12 +188,15 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
         for (int v = 0; v < NV4; ++v) acc_o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int i0 = 0; i0 < k; i0 += KB) {
             if (i0 > 0) load_batch(i0);
+            float w_at = my_w[0];  // pieces [i0, i0 + KB) are in one group of 32
+#pragma unroll
+            for (int h = 1; h < kHeld; ++h) w_at = i0 >= 32 * h ? my_w[h] : w_at;
 #pragma unroll
             for (int j = 0; j < KB; ++j) {
                 const int i = i0 + j;
                 if (i < k) {
-                    const float w = i < 32 ? __shfl_sync(0xffffffffu, my_w, i)
-                                           : expf(args.part_lse[prow_of(i)] - m) * inv;
+                    const float w = i < 32 * kHeld ? __shfl_sync(0xffffffffu, w_at, i & 31)
+                                                   : expf(args.part_lse[prow_of(i)] - m) * inv;
 #pragma unroll
                     for (int v = 0; v < NV4; ++v) {
                         acc_o[v].x += w * x[j][v].x;

@@ -88,6 +88,8 @@ struct PagedLens {
     const PagedArgs* a;  // the kernel's own parameter
     __device__ __forceinline__ int operator()(int b) const { return view_of(*a, paged_len(*a, b)).rows; }
     __device__ __forceinline__ int cut() const { return a->cut_tiles; }
+    // (where whole sequences leave partials, the merge knows whole and balanced runs only)
+    __device__ __forceinline__ bool even() const { return a->whole_slot < 0; }
 };
 
 // Rows seen by one query token: [0, f) and [b0, b1).
