@@ -540,10 +540,17 @@ __global__ void __launch_bounds__(192, 1)
                 const int e = q_row_exponent(amax);
                 if (qpart == 0) qscale[qj] = ldexpf(args.scale_log2, -e);
                 const float up = ldexpf(1.f, e);
+                // the terms in three rounds, the units read again (unrolled over all
+                // units this was 1700 instructions, fetched anew for each piece)
+                constexpr int kQRound = kQUnits / 3;
+                static_assert(3 * kQRound == kQUnits, "q units per round");
+#pragma unroll 1
+                for (int round = 0; round < 3; ++round)
 #pragma unroll
-                for (int i = 0; i < kQUnits; ++i) {
-                    const int sg = qpart + i * kThrPerRow;
-                    const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+                for (int i = 0; i < kQRound; ++i) {
+                    const int sg = qpart + (round * kQRound + i) * kThrPerRow;
+                    const uint4 qu = __ldg(qrow + sg);
+                    const uint32_t w[4] = {qu.x, qu.y, qu.z, qu.w};
                     float x[8];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {

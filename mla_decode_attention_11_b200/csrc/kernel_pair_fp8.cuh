@@ -652,14 +652,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 const int e = q_row_exponent(amax);
                 if (h == 0) qscale[r] = ldexpf(1.f, -e);
                 const float up = ldexpf(1.f, e);
+                constexpr int kQRound = 4;
 #pragma unroll 1
-                for (int bt = kQBatches - 1; bt >= 0; --bt) {
-                    if (bt != kQBatches - 1) {
+                for (int bt = 0; bt < kQUnits / kQRound; ++bt) {
 #pragma unroll
-                        for (int i = 0; i < kQBatch; ++i) qv[i] = __ldg(qsrc + bt * kQBatch + i);
-                    }
+                    for (int i = 0; i < kQRound; ++i) qv[i] = __ldg(qsrc + bt * kQRound + i);
 #pragma unroll
-                    for (int i = 0; i < kQBatch; ++i) {
+                    for (int i = 0; i < kQRound; ++i) {
                         const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
                         float x[8];
 #pragma unroll
@@ -685,7 +684,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                             }
                         }
                         // codes d0 .. d0+7 of chunk d0 / 64: half of one 16-byte unit of row r
-                        const int d0 = (kQUnits * h + bt * kQBatch + i) * 8;
+                        const int d0 = (kQUnits * h + bt * kQRound + i) * 8;
                         const uint32_t u = static_cast<uint32_t>((d0 % kChunk) / 16);
                         const uint32_t half8 = static_cast<uint32_t>((d0 % 16) / 8) * 8;
 #pragma unroll
