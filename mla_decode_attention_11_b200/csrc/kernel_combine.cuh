@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
     mla_prefix_combine_kernel(const PrefixCombineArgs args, const __grid_constant__ PagedArgs own,
                               const __grid_constant__ PagedArgs pre) {
     constexpr int NV4 = kDv / 128;
+    constexpr int kHeld = 3;  // weights a lane keeps, one for every 32 pieces
     __shared__ int s_split;
     __shared__ long long s_acc, s_tot;
     const int b = blockIdx.x;
@@ -318,31 +319,45 @@ __global__ void __launch_bounds__(kCombineThreads, 2)
             }
         };
         load_batch(0);
-        const float my_l = lane < k ? lse_of(lane) : -INFINITY;
-        float m = my_l;
-        for (int i = lane + 32; i < k; i += 32) m = fmaxf(m, lse_of(i));
+        float my_w[kHeld];
+        float m = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+            my_w[h] = lane + 32 * h < k ? lse_of(lane + 32 * h) : -INFINITY;
+            m = fmaxf(m, my_w[h]);
+        }
+        for (int i = lane + 32 * kHeld; i < k; i += 32) m = fmaxf(m, lse_of(i));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         m = fmaxf(m, sink);
         if (m == -INFINITY) m = 0.f;  // nothing to see and no sink: out = 0, lse = -inf
-        const float my_e = lane < k ? expf(my_l - m) : 0.f;
-        float sum = my_e;
-        for (int i = lane + 32; i < k; i += 32) sum += expf(lse_of(i) - m);
+        float sum = 0.f;
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+            my_w[h] = lane + 32 * h < k ? expf(my_w[h] - m) : 0.f;
+            sum += my_w[h];
+        }
+        for (int i = lane + 32 * kHeld; i < k; i += 32) sum += expf(lse_of(i) - m);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         sum += expf(sink - m);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const float my_w = my_e * inv;
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) my_w[h] *= inv;
         float4 acc_o[NV4];
 #pragma unroll
         for (int v = 0; v < NV4; ++v) acc_o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int i0 = 0; i0 < k; i0 += 4) {
             if (i0 > 0) load_batch(i0);
+            float w_at = my_w[0];
+#pragma unroll
+            for (int h = 1; h < kHeld; ++h) w_at = i0 >= 32 * h ? my_w[h] : w_at;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int i = i0 + j;
                 if (i < k) {
-                    const float w = i < 32 ? __shfl_sync(0xffffffffu, my_w, i) : expf(lse_of(i) - m) * inv;
+                    const float w = i < 32 * kHeld ? __shfl_sync(0xffffffffu, w_at, i & 31)
+                                                   : expf(lse_of(i) - m) * inv;
 #pragma unroll
                     for (int v = 0; v < NV4; ++v) {
                         acc_o[v].x += w * x[j][v].x;

@@ -57,12 +57,13 @@ PrefixLayout prefix_layout(const mla_plan& pl) {
 // a time.  With 128 rows a sequence both do the same products, and one launch
 // balances them together and leaves no partial of a sequence that is not cut.
 // With fewer, a sequence's own pass over the prefix takes NG / 148 of its tiles'
-// time each; up to 4 tiles (about 12 us) a CTA that is less than the second
-// launch and the partials cost (about 20 us).
+// time each, about 2.7 us a tile of a CTA, and the second launch and the partials
+// some 20 us: the two are level at 8 tiles a CTA (64 sequences, 16 heads: 41 and
+// 41 us; at 4 29 and 39, at 16 64 and 45).
 bool prefix_in_front(const mla_plan& pl) {
     if (pl.kernel == MLA_KERNEL_PAIR) return true;
     const int64_t tiles = (static_cast<int64_t>(pl.prefix_max) + mla::kTileKV - 1) / mla::kTileKV;
-    return tiles * pl.B * pl.num_groups <= 4 * static_cast<int64_t>(pl.num_sms);
+    return tiles * pl.B * pl.num_groups <= 8 * static_cast<int64_t>(pl.num_sms);
 }
 
 // Latent pages [num_pages, page_size, 576]: boxes of `rows` rows x 64 columns x
