@@ -60,42 +60,47 @@ struct AppendArgs {
 constexpr int kAppendThreads = 128;
 constexpr int kAppendRowBytes = 2048;  // head-row bytes of one task
 
-// The sequence of token i (cu[b] <= i < cu[b+1]), or -1; warp-cooperative.
-// Each round narrows the range 32-fold: the lanes read evenly spaced bounds
-// and the last one at most i opens the next range.
-__device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int i, int lane) {
-    int lo = 0, n = B + 1;  // the answer's index is in [lo, lo + n)
-    while (n > 1) {
-        const int step = (n + 31) >> 5;
-        const int at = lane * step;
-        const bool le = at < n && __ldg(cu + lo + at) <= i;
-        const unsigned m = __ballot_sync(0xffffffffu, le);
-        if (m == 0) return -1;
-        const int last = 31 - __clz(m);
-        lo += last * step;
-        n = n - last * step < step ? n - last * step : step;
-    }
-    return lo < B && __ldg(cu + lo) <= i && i < __ldg(cu + lo + 1) ? lo : -1;
-}
-
 // Sequence and position of token i; position -1: the token is in no sequence
-// (padding) or its position is outside [0, num_positions) (flagged).
+// (padding) or its position is outside [0, num_positions) (flagged).  Warp-
+// cooperative: each round of the search narrows the bounds 32-fold (the lanes read
+// evenly spaced ones, and the last at most i opens the next range), and the last
+// round reads the lengths with them, so that a token's chain of loads is one
+// shorter.
 __device__ __forceinline__ void place_token(const AppendArgs& a, int i, int lane, int& b, int& pos) {
-    int first, n;
+    long long next, L;
     if (a.cu) {
-        b = sequence_of(a.cu, a.B, i, lane);
-        if (b < 0) {
+        int lo = 0, n = a.B + 1;  // the answer is in [lo, lo + n)
+        while (n > 32) {
+            const int step = (n + 31) >> 5;
+            const int at = lane * step;
+            const unsigned m = __ballot_sync(0xffffffffu, at < n && __ldg(a.cu + lo + at) <= i);
+            if (m == 0) break;
+            const int last = 31 - __clz(m);
+            lo += last * step;
+            n = n - last * step < step ? n - last * step : step;
+        }
+        const int at = lo + lane;
+        int opens = 0, closes = 0, len = 0;
+        if (lane < n && at < a.B) {
+            opens = __ldg(a.cu + at);
+            closes = __ldg(a.cu + at + 1);
+            len = __ldg(a.seqlens + at);
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, lane < n && at < a.B && opens <= i);
+        const int last = m == 0 ? 0 : 31 - __clz(m);
+        b = lo + last;
+        next = __shfl_sync(0xffffffffu, closes, last);
+        L = __shfl_sync(0xffffffffu, len, last);
+        if (m == 0 || i >= next) {
             pos = -1;
             return;
         }
-        first = __ldg(a.cu + b);
-        n = __ldg(a.cu + b + 1) - first;
     } else {
         b = i / a.per_seq;
-        first = b * a.per_seq;
-        n = a.per_seq;
+        next = static_cast<long long>(b + 1) * a.per_seq;
+        L = __ldg(a.seqlens + b);
     }
-    const long long p = static_cast<long long>(__ldg(a.seqlens + b)) - n + (i - first);
+    const long long p = L - next + i;
     pos = -1;
     if (p >= 0 && p < a.num_positions) pos = static_cast<int>(p);
     else if (a.status && lane == 0) atomicOr(a.status, kStatusSeqlen);
