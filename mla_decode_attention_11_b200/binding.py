@@ -157,7 +157,8 @@ def load_library(build_if_missing: bool = True):
         lib.mla_cache_append.argtypes = [c_vp, c_vp]
         lib.mha_cache_append.argtypes = [c_vp, c_vp]
         for fn in (lib.mla_decode_plan_paged, lib.mha_decode_plan_paged, lib.mla_decode_plan_prefix,
-                   lib.mla_decode_plan_paged_fp8, lib.mla_decode_run_paged_fp8, lib.mla_decode_run_paged, lib.mha_decode_run_paged, lib.mla_decode_run_prefix,
+                   lib.mla_decode_plan_paged_fp8, lib.mla_decode_run_paged_fp8, lib.mla_decode_run_paged,
+                   lib.mha_decode_run_paged, lib.mla_decode_run_prefix,
                    lib.mla_cache_append, lib.mha_cache_append):
             fn.restype = c_i32
         lib.mla_decode_check.restype = c_i32
@@ -743,18 +744,18 @@ def _query_rows(q_in, q_out, in_name, out_name, T, width, out_width, device):
     return H, in_strides, out_strides
 
 
-def _append(name, device, T, H, Hkv, k, v, cos_sin, k_pages, v_pages, block_table, seqlens, cu_tokens, q_in, q_out,
+def _append(name, device, T, H, Hkv, k, v, cos_sin, rot, k_pages, v_pages, block_table, seqlens, cu_tokens, q_in, q_out,
             q_out_offset, strides, kv_scale, interleaved, workspace, stream):
     B = seqlens.shape[0]
     _check_on(seqlens, "seqlens", torch.int32, (B,), device)
     _check_table(block_table, "block_table", B, device)
-    positions, rot = cos_sin.shape
+    positions = cos_sin.shape[0]
     _check_on(cos_sin, "cos_sin", torch.float32, (positions, rot), device)
     if cu_tokens is not None:
         _check_on(cu_tokens, "cu_tokens", torch.int32, (B + 1,), device)
     if workspace is not None:
         _check_workspace(workspace, device)
-    pages, page_size = k_pages.shape[:2]
+    pages, page_size = k_pages.shape[0], k_pages.shape[1]
     args = _APPEND.pack(
         B, T, H, Hkv, rot, 1 if interleaved else 0, positions, page_size, pages, block_table.shape[1],
         block_table.stride()[0], cu_tokens.data_ptr() if cu_tokens is not None else 0, seqlens.data_ptr(),
@@ -762,15 +763,15 @@ def _append(name, device, T, H, Hkv, k, v, cos_sin, k_pages, v_pages, block_tabl
         q_out.data_ptr() + q_out_offset if H else 0, k_pages.data_ptr(),
         v_pages.data_ptr() if v_pages is not None else 0, *strides,
         workspace.data_ptr() if workspace is not None else 0, kv_scale, 0)
-    rc = getattr(load_library(), name)(args, _stream_on(device, stream))
+    rc = getattr(_lib or load_library(), name)(args, _stream_on(device, stream))
     if rc != MLA_OK:
         raise MlaError(rc, name)
 
 
-def _check_cos_sin(cos_sin: torch.Tensor, columns: Optional[int]) -> None:
-    if cos_sin.dim() != 2 or (columns is not None and cos_sin.shape[1] != columns):
-        raise ValueError(f"cos_sin must have shape (positions, {columns or 'rotated columns'}), "
-                         f"got {tuple(cos_sin.shape)}")
+def _paged_shape(pages: torch.Tensor, *row) -> Tuple[int, ...]:
+    """(pages, page_size, *row), with the first two those of the tensor."""
+    shape = pages.shape
+    return (shape[0], shape[1], *row) if len(shape) > 1 else row
 
 
 def mla_cache_append(latent: torch.Tensor, k_rope: torch.Tensor, cos_sin: torch.Tensor, kv_pages: torch.Tensor,
@@ -796,11 +797,10 @@ def mla_cache_append(latent: torch.Tensor, k_rope: torch.Tensor, cos_sin: torch.
         raise ValueError("kv_scale goes with a cache of E4M3 codes (torch.uint8 or torch.float8_e4m3fn)")
     if fp8 and not kv_scale > 0:
         raise ValueError("kv_scale must be positive")
-    _check_on(kv_pages, "kv_pages", kv_pages.dtype if fp8 else torch.bfloat16, (*kv_pages.shape[:2], D_QK), device)
-    _check_cos_sin(cos_sin, D_QK - D_V)
+    _check_on(kv_pages, "kv_pages", kv_pages.dtype if fp8 else torch.bfloat16, _paged_shape(kv_pages, D_QK), device)
     H, in_strides, out_strides = _query_rows(q_rope, q, "q_rope", "q", T, D_QK - D_V, D_QK, device)
-    _append("mla_cache_append", device, T, H, 1, latent, k_rope, cos_sin, kv_pages, None, block_table, seqlens,
-            cu_tokens, q_rope, q, 2 * D_V, (*k_strides, *v_strides, *in_strides, *out_strides),
+    _append("mla_cache_append", device, T, H, 1, latent, k_rope, cos_sin, D_QK - D_V, kv_pages, None,
+            block_table, seqlens, cu_tokens, q_rope, q, 2 * D_V, (*k_strides, *v_strides, *in_strides, *out_strides),
             float(kv_scale) if fp8 else 0.0, interleaved, workspace, stream)
 
 
@@ -817,9 +817,11 @@ def mha_cache_append(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor, k_
     device, T, Hkv = _device_of(k, "k"), k.shape[0], k.shape[1] if k.dim() == 3 else -1
     k_strides = _rows(k, "k", (T, Hkv, MHA_D), device)
     v_strides = _rows(v, "v", (T, Hkv, MHA_D), device)
-    _check_on(k_pages, "k_pages", torch.bfloat16, (*k_pages.shape[:2], Hkv, MHA_D), device)
+    _check_on(k_pages, "k_pages", torch.bfloat16, _paged_shape(k_pages, Hkv, MHA_D), device)
     _check_on(v_pages, "v_pages", torch.bfloat16, k_pages.shape, device)
-    _check_cos_sin(cos_sin, None)
+    if cos_sin.dim() != 2:
+        raise ValueError(f"cos_sin must have shape (positions, rotated columns), got {tuple(cos_sin.shape)}")
     H, in_strides, out_strides = _query_rows(q_in, q_out, "q_in", "q_out", T, MHA_D, MHA_D, device)
-    _append("mha_cache_append", device, T, H, Hkv, k, v, cos_sin, k_pages, v_pages, block_table, seqlens, cu_tokens,
-            q_in, q_out, 0, (*k_strides, *v_strides, *in_strides, *out_strides), 0.0, interleaved, workspace, stream)
+    _append("mha_cache_append", device, T, H, Hkv, k, v, cos_sin, cos_sin.shape[1], k_pages, v_pages, block_table,
+            seqlens, cu_tokens, q_in, q_out, 0, (*k_strides, *v_strides, *in_strides, *out_strides), 0.0, interleaved,
+            workspace, stream)

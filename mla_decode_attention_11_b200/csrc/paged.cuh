@@ -12,10 +12,10 @@
 //     i >= split: position i + jump     (boxes from the one that holds lo)
 // with jump = 0 where nothing is left out.  Behind a shared prefix of P keys the
 // rows below split = P rounded up to a box are the prefix's, found in its own
-// table, and the sequence's own keys follow with jump = -split.  Rows that no token sees -- past L,
-// and around the ends of the two ranges in their boxes -- are masked in S and
-// zeroed in shared memory before P V, so whatever they hold (a page's old
-// contents, NaN) reaches no result.  Boxes past the end are loaded with a page
+// table, and the sequence's own keys follow with jump = -split.  Rows that no
+// token sees -- past L, and around the ends of the two ranges in their boxes -- are
+// masked in S and zeroed in shared memory before P V, so whatever they hold (a
+// page's old contents, NaN) reaches no result.  Boxes past the end are loaded with a page
 // index outside the cache, which TMA fills with zeros; so is a table entry
 // outside it, which is also flagged.
 #pragma once
@@ -137,14 +137,13 @@ __device__ __forceinline__ bool tile_unseen(const PagedArgs& a, const SeqView& v
 // at a time, a lane each, and leaves them in a list of 64 in shared memory:
 // while that thread issues the tiles of one half, the entries of the next are on
 // their way.  The thread is the one elect.sync names, so that the compiler knows
-// TMA's operands to be one thread's.  Polling, arming and issuing with the whole warp instead (a box a
-// lane) cost 23 % at 128 heads and 22 % over grouped kv heads even where a tile
-// is one box or two.
+// TMA's operands to be one thread's.  Polling, arming and issuing with the whole
+// warp instead (a box a lane) cost 23 % at 128 heads and 22 % over grouped kv heads
+// even where a tile is one box or two.
 // kMost: the most boxes of a tile.
 template <class Walker, int kMost>
 struct BoxList {
     static constexpr int kEntries = 64;
-    static constexpr int kBytes = kEntries * 8;
     const PagedArgs& a;
     int2* list;          // (page, row) of each box; page num_pages: outside the cache, TMA writes zeros
     Walker w;
