@@ -707,6 +707,30 @@ def test_prefix_equals_whole_sequences(cuda_device, H, most):
     close(out2, lse2, ref)
 
 
+def test_calls_on_two_streams_at_once(cuda_device):
+    """Two-launch prefix decodes on one stream while paged decodes of every kernel run on another, each with a workspace
+    of its own: the same bits as one after the other."""
+    jobs = [make_prefix([40, 0, 300, 128] * 10, 1, 16, 900, 64, True, seed=1, prefix_max=LONG),
+            make_prefix([40, 0, 300] * 5, 1, 128, 500, 64, False, seed=2)]
+    jobs += [make_window(kind, [700, 5, 2000, 90], 1, H, Hkv, 64, 256, 4, False, 3)
+             for kind, H, Hkv in (("mla", 16, 1), ("mla", 128, 1), ("mla_fp8", 32, 1), ("mla_fp8", 128, 1), ("mha", 8, 2))]
+    alone = []
+    for run, ref, (out, lse), (plan, ws, *_) in jobs:
+        run(out, lse)
+        M.mla_decode_check(plan, ws)
+        alone.append((out.clone(), lse.clone()))
+    streams = [torch.cuda.Stream(DEV), torch.cuda.Stream(DEV)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, (run, ref, (out, lse), _) in enumerate(jobs):
+            with torch.cuda.stream(streams[0 if i < 2 else 1]):
+                run(out, lse)
+    torch.cuda.synchronize()
+    for (run, ref, (out, lse), (plan, ws, *_)), (o, l) in zip(jobs, alone):
+        M.mla_decode_check(plan, ws)
+        assert torch.equal(out, o) and torch.equal(lse, l)
+
+
 def test_refusals(cuda_device):
     pages = Pages("mla", [64, 64], 16)
     plan = M.mla_decode_plan_paged(2, 1, 16, 64, 16, device=0)
