@@ -324,7 +324,9 @@ __global__ void __launch_bounds__(kAppendThreads) mha_cache_append_kernel(const 
         return k;
     };
     auto load = [&](R& rows, const Task& k) {
-        const __nv_bfloat16* from = k.kind == 0 ? a.k + i * a.k_token : k.kind == 1 ? a.v + i * a.v_token : a.q_in + i * a.qi_token;
+        const __nv_bfloat16* from = k.kind == 0   ? a.k + i * a.k_token
+                                    : k.kind == 1 ? a.v + i * a.v_token
+                                                  : a.q_in + i * a.qi_token;
         const long long step = k.kind == 0 ? a.k_head : k.kind == 1 ? a.v_head : a.qi_head;
         rows.load(from + k.h0 * step, step, k.n, lane);
     };

@@ -141,7 +141,8 @@ mla_status check_paged(const mla_plan* plan, const void* q, const void* k, const
     const mla_plan& pl = *plan;
     if (pl.B < 1 || pl.Sq < 1 || pl.H < 1 || pl.Hkv < 1 || pl.L_max < 1 || pl.num_partitions < 1 ||
         pl.num_partitions > 4096 || pl.num_groups < 1 || pl.split_tiles != 0 || pl.l2_prefetch_tiles < 0 ||
-        pl.l2_prefetch_tiles > 16 || pl.page_size < 1 || check_page_args(pl.page_size, pl.window, pl.first_tokens) != MLA_OK)
+        pl.l2_prefetch_tiles > 16 || pl.page_size < 1 ||
+        check_page_args(pl.page_size, pl.window, pl.first_tokens) != MLA_OK)
         return MLA_ERR_INVALID_ARG;
     if (num_pages < 1 || table_stride < 0 || table_width < 1 ||
         static_cast<int64_t>(table_width) * pl.page_size < pl.L_max)
@@ -525,7 +526,8 @@ mla_status mla_decode_run_prefix(const mla_plan* plan, const void* q, const void
     c.pre_o = ap.part_o;
     c.pre_lse = ap.part_lse;
     c.sinks = sinks;
-    return launch_dependent(mla::mla_prefix_combine_kernel, combine_grid(pl), mla::kCombineThreads, stream, 0, c, po, pp);
+    return launch_dependent(mla::mla_prefix_combine_kernel, combine_grid(pl), mla::kCombineThreads, stream, 0, c, po,
+                            pp);
 }
 
 }  // extern "C"

@@ -6,11 +6,11 @@ Tolerances.  Scores accumulate n products of the key's width in fp32, so each is
 n 2^-24 scale sum |q k| =: delta (first order), and so is lse; its sum and its logarithm add a few 2^-23 of its value.
 The weights a row multiplies its values with are rounded to bf16 (2^-8 relative; E4M3 pages: two E4M3 terms, 2^-4 of
 2^-4, of a weight rounded to f16 at most, 2^-11, and 2^-14 of the largest weight where the second term has no more
-bits), so with A = sum p |v| an output is off
-by at most (2^-8 + 2 delta) A, and by 2^-8 of itself from its own rounding.  2^-20 stands for the fp32 steps of the
-merges.  E4M3 pages: a query row, scaled so that its largest element is in [224, 448], is carried as two or three E4M3
-terms.  Two hold the 8 bits of a bf16 exactly unless its last bit is below E4M3's smallest step 2^-9, and are off by half
-of that otherwise: 2^-10 / 224 of the row's largest element, in each of the products.  Rows of a page that no token sees hold NaN (or the NaN code), and so do outputs before a call.
+bits), so with A = sum p |v| an output is off by at most (2^-8 + 2 delta) A, and by 2^-8 of itself from its own rounding.
+2^-20 stands for the fp32 steps of the merges.  E4M3 pages: a query row, scaled so that its largest element is in
+[224, 448], is carried as two or three E4M3 terms.  Two hold the 8 bits of a bf16 exactly unless its last bit is below
+E4M3's smallest step 2^-9, and are off by half of that otherwise: 2^-10 / 224 of the row's largest element, in each of the
+products.  Rows of a page that no token sees hold NaN (or the NaN code), and so do outputs before a call.
 """
 import math
 
