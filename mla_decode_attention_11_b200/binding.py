@@ -755,6 +755,8 @@ def _append(name, device, T, H, Hkv, k, v, cos_sin, rot, k_pages, v_pages, block
         _check_on(cu_tokens, "cu_tokens", torch.int32, (B + 1,), device)
     if workspace is not None:
         _check_workspace(workspace, device)
+        if workspace.data_ptr() == 0 or workspace.nbytes < 256:
+            raise ValueError("workspace must be a decode plan's workspace")
     pages, page_size = k_pages.shape[0], k_pages.shape[1]
     args = _APPEND.pack(
         B, T, H, Hkv, rot, 1 if interleaved else 0, positions, page_size, pages, block_table.shape[1],
@@ -795,8 +797,8 @@ def mla_cache_append(latent: torch.Tensor, k_rope: torch.Tensor, cos_sin: torch.
     fp8 = kv_pages.dtype in (torch.uint8, torch.float8_e4m3fn)
     if fp8 != (kv_scale is not None):
         raise ValueError("kv_scale goes with a cache of E4M3 codes (torch.uint8 or torch.float8_e4m3fn)")
-    if fp8 and not kv_scale > 0:
-        raise ValueError("kv_scale must be positive")
+    if fp8 and not 2.0 ** -149 <= kv_scale < 2.0 ** 127:  # 0 in fp32 would ask for bf16 rows
+        raise ValueError("kv_scale must be positive and finite in fp32")
     _check_on(kv_pages, "kv_pages", kv_pages.dtype if fp8 else torch.bfloat16, _paged_shape(kv_pages, D_QK), device)
     H, in_strides, out_strides = _query_rows(q_rope, q, "q_rope", "q", T, D_QK - D_V, D_QK, device)
     _append("mla_cache_append", device, T, H, 1, latent, k_rope, cos_sin, D_QK - D_V, kv_pages, None,

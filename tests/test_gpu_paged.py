@@ -796,3 +796,23 @@ def test_refusals(cuda_device):
     for n in (8, 24, 136):
         with pytest.raises(M.MlaError):
             M.mha_cache_append(heads, heads, torch.zeros(64, n, device=DEV), kp, kp.clone(), pages.table, sl)
+
+
+def test_append_refuses_scales_and_workspaces(cuda_device):
+    """An E4M3 cache's scale that fp32 cannot hold is refused (rounded to 0 it would stand for a cache of bf16 rows,
+    twice as long), and a workspace without room for the status words."""
+    table, sl = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.tensor([1], dtype=torch.int32, device=DEV)
+    row = torch.ones(1, 576, dtype=torch.bfloat16, device=DEV)
+    codes = torch.full((2, 16, 576), 0x55, dtype=torch.uint8, device=DEV)
+    call = lambda **kw: M.mla_cache_append(row[:, :512], row[:, 512:], M.rope_table(16, 64, device=DEV),
+                                           codes, table, sl, **kw)
+    for bad in (0.0, -1.0, math.nan, math.inf, 1e-60, 1e-46, 1e60, None):
+        with pytest.raises(ValueError):
+            call(kv_scale=bad)
+    for words in (0, 63):
+        with pytest.raises(ValueError):
+            call(kv_scale=1.0, workspace=torch.zeros(words, dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    assert bool((codes == 0x55).all())
+    call(kv_scale=2.0 ** -149)
+    assert bool((codes[0, 0] == 0x7E).sum() >= 512) and bool((codes[0, 1:] == 0x55).all()) and bool((codes[1] == 0x55).all())
