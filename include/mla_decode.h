@@ -535,7 +535,8 @@ mla_status mla_decode_run_prefix(const mla_plan* plan, const void* q, const void
  * left alone.  A token whose position is outside [0, num_positions) is skipped
  * and flagged (MLA_ERR_SEQLEN); one whose page is outside the table's width or
  * [0, num_pages) has its queries rotated, its cache row not written, and is
- * flagged (MLA_ERR_PAGE).  Two tokens with the same place leave either's row.
+ * flagged (MLA_ERR_PAGE).  Tokens with the same
+ * place leave a row of parts of theirs.
  */
 typedef struct mla_append {
     int32_t B, T;               /* sequences (>= 1), new tokens of all of them (>= 0) */

@@ -816,3 +816,65 @@ def test_append_refuses_scales_and_workspaces(cuda_device):
     assert bool((codes == 0x55).all())
     call(kv_scale=2.0 ** -149)
     assert bool((codes[0, 0] == 0x7E).sum() >= 512) and bool((codes[0, 1:] == 0x55).all()) and bool((codes[1] == 0x55).all())
+
+
+@pytest.mark.parametrize("kind", ["mla", "mla_fp8", "mha"])
+def test_offsets_beyond_32_bits(cuda_device, kind):
+    """Pages at the end of a cache of more than 2^32 elements (E4M3: bytes) and a block table whose rows are more than
+    2^31 entries apart: append and decode give the bits of a small cache."""
+    page, H, Hkv, lengths = 64, 16, 8, [200, 130]
+    row = (Hkv, 128) if kind == "mha" else (576,)
+    dtype = torch.uint8 if kind == "mla_fp8" else torch.bfloat16
+    num = 2 ** 32 // (page * math.prod(row)) + 10
+    # the table's rows lie in one buffer: entries 0.. and 2^31 + 16..
+    wide = torch.empty(2 ** 31 + 32, dtype=torch.int32, device=DEV).as_strided((2, 4), (2 ** 31 + 16, 1))
+    wide.copy_(torch.arange(num - 8, num, dtype=torch.int32).view(2, 4))
+    near = torch.arange(8, dtype=torch.int32, device=DEV).view(2, 4)
+    sl = torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, lengths[0], sum(lengths)], dtype=torch.int32, device=DEV)
+    T = sum(lengths)
+    g = torch.Generator(device=DEV).manual_seed(7)
+    rand = lambda *shape: torch.randn(*shape, dtype=torch.bfloat16, device=DEV, generator=g)
+    cos_sin = M.rope_table(256, 128 if kind == "mha" else 64, device=DEV)
+    k, v, q = rand(T, *((Hkv, 128) if kind == "mha" else (512,))), rand(T, *((Hkv, 128) if kind == "mha" else (64,))), \
+        rand(2, 1, H, 128 if kind == "mha" else 576)
+    results = []
+    for table, pages in ((near, 8), (wide, num)):
+        out, lse = blank(2, 1, H, 128 if kind == "mha" else 512)
+        caches = [torch.empty(pages, page, *row, dtype=dtype, device=DEV) for _ in range(2 if kind == "mha" else 1)]
+        if kind == "mha":
+            plan = M.mha_decode_plan_paged(2, 1, H, Hkv, 256, page, device=0)
+            ws = M.alloc_workspace(plan)
+            M.mha_cache_append(k, v, cos_sin, *caches, table, sl, cu, workspace=ws)
+            M.mha_decode_run_paged(plan, q, *caches, table, sl, 0.1, out, lse, ws)
+        elif kind == "mla":
+            plan = M.mla_decode_plan_paged(2, 1, H, 256, page, device=0)
+            ws = M.alloc_workspace(plan)
+            M.mla_cache_append(k, v, cos_sin, *caches, table, sl, cu, workspace=ws)
+            M.mla_decode_run_paged(plan, q, *caches, table, sl, 0.05, out, lse, ws)
+        else:
+            plan = M.mla_decode_plan_paged_fp8(2, 1, H, 256, page, device=0)
+            ws = M.alloc_workspace(plan)
+            M.mla_cache_append(k, v, cos_sin, *caches, table, sl, cu, kv_scale=0.02, workspace=ws)
+            M.mla_decode_run_paged_fp8(plan, q, *caches, 0.02, table, sl, 0.05, out, lse, ws)
+        M.mla_decode_check(plan, ws)
+        held = torch.cat([c[-8:].view(torch.uint8).view(2, 4 * page, -1)[b, :n] for c in caches for b, n in enumerate(lengths)])
+        results.append((out, lse, held.clone()))
+        del caches
+    for small, large in zip(*results):
+        assert torch.equal(small, large)
+    assert bool(results[0][0].isfinite().all())
+
+
+def test_tokens_with_the_same_place(cuda_device):
+    """Two sequences that append to the same row of the same page: every element of it is one of theirs, and nothing else
+    changes."""
+    table = torch.zeros(2, 1, dtype=torch.int32, device=DEV)
+    sl = torch.tensor([3, 3], dtype=torch.int32, device=DEV)
+    x = torch.arange(1, 3, dtype=torch.bfloat16, device=DEV)[:, None].expand(2, 576).contiguous()
+    angles = torch.cat([torch.ones(16, 32), torch.zeros(16, 32)], 1).to(DEV)  # no rotation
+    kv = torch.zeros(2, 16, 576, dtype=torch.bfloat16, device=DEV)
+    M.mla_cache_append(x[:, :512], x[:, 512:], angles, kv, table, sl)
+    assert bool(((kv[0, 2] == 1) | (kv[0, 2] == 2)).all())
+    kv[0, 2] = 0
+    assert not bool(kv.any())
