@@ -360,8 +360,11 @@ mla_status mha_decode_run_phase(const mla_plan* plan, const void* q, const void*
  *   MLA_KERNEL_FP8_MMA (the default otherwise): the codes are the operands of
  *     kind::f8f6f4 tensor-core MMAs as they are; each q row is scaled by a
  *     power of two and carried as the sum of three E4M3 terms (about 12
- *     significant bits, relative error <= 2^-12), and P (scaled by 2^4) as the
- *     sum of two (about 8 bits, the precision of the bf16 P of the bf16 path).
+ *     significant bits, relative error <= 2^-12), and P as the sum of two: each
+ *     weight to about 8 bits (the precision of the bf16 P of the bf16 path), and
+ *     what falls below the terms' smallest step, however many keys that is, to
+ *     2^-7 of a row's weights at most.  lse sums the weights before their
+ *     rounding and is as exact as the scores.
  *   MLA_KERNEL_FP8: every E4M3 value divided by 2^8 is exact in f16, so the
  *     kernel widens the codes to those f16 values in shared memory (integer
  *     bit moves) and runs f16 x f16 -> f32 MMAs; q is narrowed from bf16 to f16

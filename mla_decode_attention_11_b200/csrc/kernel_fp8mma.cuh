@@ -14,16 +14,27 @@
 //      [0, G), [G, 2G), [2G, 3G) of one S^T MMA, so every K tile is read
 //      once:  S^T[kv, j] = (sum_k S^T_k[kv, j]) * 2^-e_j.
 //   P: scaled by 2^4 and written as the sum of two E4M3 terms (about 8
-//      significant bits, the precision of the bf16 P of the other kernels);
-//      the two terms are the N columns [0, G) and [G, 2G) of the PV MMAs,
-//      O^T = O^T_1 + O^T_2.  The reference max is raised only when a column's
+//      significant bits, the precision of the bf16 P of the other kernels):
+//      t1 = e4m3(2^4 p), t2 = e4m3(2^5 (2^4 p - t1)) with a scale of its own,
+//      which keeps it in E4M3's normal range where t1's remainder is small.
+//      The two terms are the N columns [0, G) and [G, 2G) of the PV MMAs,
+//      O^T = O^T_1 + 2^-5 O^T_2.  The reference max m is raised when a column's
 //      max exceeds it by more than 4 (base 2), so 2^4 p <= 256 stays inside
-//      E4M3 while weights down to 2^-10 of the reference keep normal codes
-//      (at scale 1 the smaller ones would fall into the subnormal range and
-//      lose precision; a threshold of 1 with 2^7 p rescaled O far more often).
+//      E4M3 (and 2^5 times its remainder, at most 8).
+//
+// What the terms lose.  A key's 2^4 p is off by at most 2^-8 of itself, and by
+// 2^-14 where t1 has no normal code (below 2^-6): in p, 128 * 2^-18 = 2^-11 of
+// 2^m for a whole tile.  Thousands of keys below a dominant one that came first
+// can be worth as much as it is and still each be below that step.  So for each
+// query row a lane of every warp weighs the tiles, each by its maximum: at one
+// far below the reference, where 2^-11 a tile so far is more than 2^-7 of that
+// weight, the reference goes down to the tile's maximum (O and the sums are fp32
+// and scale up).  In all, then, the step loses at most 2^-7 of a row's weights.
+// On scores of N(0, 2^2) nats this moves references hardly more often than raising
+// them alone; counting only tiles, without their weights, cost 10 %.
 //
 // K and V are exact; the errors are the truncation of q (<= 2^-12 relative)
-// and of p (<= 2^-8 relative), and fp32 accumulation.  A host-side emulation
+// and of p (as above), and fp32 accumulation.  A host-side emulation
 // of these splits on N(0, 1) and N(0, 9) data gives out rel-L2 ~1.7e-3 and lse
 // errors below 1e-5 against the fp64 oracle.  Everything else --
 // the split-KV schedule, the lazy base-2 softmax, sinks, the partials and
@@ -95,9 +106,12 @@ struct Fp8MmaCfg {
     // kind::f8f6f4 with E4M3 A and B: format codes 0, the same bit layout as f16
     static constexpr uint32_t kIdescS = ptx::make_idesc_f16(128, NS, 0, 0);
     static constexpr uint32_t kIdescPV = ptx::make_idesc_f16(128, NO, 1, 1);
-    static constexpr float kLazy = 4.f;      // rescale threshold (base-2 units): p <= 16
+    static constexpr float kLazy = 4.f;      // a tile's max is near the reference within this (base-2 units): p <= 16
     static constexpr float kPScaleLog2 = 4.f;  // P is carried as 2^4 p <= 256
     static constexpr float kPScaleInv = 1.f / 16.f;
+    static constexpr float kT2Scale = 32.f;  // of the second term
+    static constexpr float kT2Inv = 1.f / 32.f;
+    static constexpr float kMaxLoss = 16.f;  // 2^-7 of a row's weights, in tiles' losses of 2^-11 of the reference
 };
 
 // D[tmem] (+)= A[smem] . B[smem], both E4M3, K = 32 per instruction.
@@ -599,6 +613,9 @@ __global__ void __launch_bounds__(192, 1)
                 all_f = least.f;
                 all_hi = least.b1;
             }
+            // of column lane % G: its reference, the highest one so far, and what its tiles may
+            // still lose (in tiles)
+            float own_m = 0.f, own_top = 0.f, own_left = 0.f;
             float m_ref[G];
             float l_part[G];
 #pragma unroll
@@ -662,14 +679,28 @@ __global__ void __launch_bounds__(192, 1)
                     tmax[j + 2] = fmaxf(fmaxf(a.z, b1.z), fmaxf(b2.z, b3.z));
                     tmax[j + 3] = fmaxf(fmaxf(a.w, b1.w), fmaxf(b2.w, b3.w));
                 }
-                // lazy rescale (threshold kLazy, so 2^4 p <= 256 < 448), uniform branch
-                bool grow = false;
+                // lazy rescale: up past kLazy (so 2^4 p <= 256 < 448), down at a tile far
+                // below when nothing is left to lose (not further than 40 below the top:
+                // so no sum leaves fp32's range); a uniform branch
+                const float* own = redmax + (lane & (G - 1));
+                const float own_t = fmaxf(fmaxf(own[0], own[G]), fmaxf(own[2 * G], own[3 * G]));
+                const float own_w = ex2_approx(own_t - own_m);
+                own_left = fmaf(C::kMaxLoss, own_w, own_left) - fminf(1.f, 0x1p18f * own_w);
+                const bool own_low = own_left < 0.f && own_t < own_m - C::kLazy && own_t > own_top - 40.f;
+                const uint32_t low = __ballot_sync(0xffffffffu, own_low);
+                bool move = !first && low != 0;
 #pragma unroll
-                for (int j = 0; j < G; ++j) grow |= (tmax[j] > m_ref[j] + C::kLazy);
+                for (int j = 0; j < G; ++j) move |= (tmax[j] > m_ref[j] + C::kLazy);
                 if (first) {
+                    own_m = own_top = CV::kPaged ? fmaxf(own_t, kNoKey) : own_t;
+                    own_left = C::kMaxLoss - 1.f;
 #pragma unroll
                     for (int j = 0; j < G; ++j) m_ref[j] = CV::kPaged ? fmaxf(tmax[j], kNoKey) : tmax[j];
-                } else if (grow) {
+                } else if (move) {
+                    const float m = own_low ? own_t : fmaxf(own_m, own_t);
+                    if (m != own_m) own_left = C::kMaxLoss - 1.f;  // the tile weighs 2^m
+                    own_m = m;
+                    own_top = fmaxf(own_top, m);
                     // O^T must hold the previous tile's PV before it is rescaled (this
                     // tile's PV waits for the P written below)
                     ok = ptx::mbar_wait_bounded(pv_tile + ((tile_cnt - 1) & 1), ((tile_cnt - 1) >> 1) & 1, tmo);
@@ -678,7 +709,7 @@ __global__ void __launch_bounds__(192, 1)
                     float alpha[G];
 #pragma unroll
                     for (int j = 0; j < G; ++j) {
-                        const float mn = fmaxf(m_ref[j], tmax[j]);
+                        const float mn = low >> j & 1 ? tmax[j] : fmaxf(m_ref[j], tmax[j]);
                         alpha[j] = ex2_approx(m_ref[j] - mn);
                         m_ref[j] = mn;
                         l_part[j] *= alpha[j];
@@ -699,7 +730,7 @@ __global__ void __launch_bounds__(192, 1)
                     }
                     ptx::tmem_wait_st();
                 }
-                // P terms of this kv row: 2^4 p = t1 + t2 (E4M3), t1 in bytes [0, G), t2 in [G, 2G);
+                // P terms of this kv row: 2^4 p = t1 + 2^-5 t2 (E4M3), t1 in bytes [0, G), t2 in [G, 2G);
                 // P buffer sb was last read by the PV of tile - 2, which the tensor pipe ran
                 // before this tile's S^T
                 uint8_t* p_buf = p_smem + sb * C::kPBytes;
@@ -710,12 +741,11 @@ __global__ void __launch_bounds__(192, 1)
                     const float p1 = ex2_approx(x[j + 1] - m_ref[j + 1] + C::kPScaleLog2);
                     const uint32_t t1 = f32x2_to_e4m3x2(p0, p1);
                     const float2 v1 = e4m3x2_to_f32x2(t1);
-                    const uint32_t t2 = f32x2_to_e4m3x2(p0 - v1.x, p1 - v1.y);
-                    const float2 v2 = e4m3x2_to_f32x2(t2);
-                    // the weights the MMAs use; in pages the weights before their rounding, so
-                    // that the lse of a few keys is as exact as its scores are
-                    l_part[j] += CV::kPaged ? p0 : v1.x + v2.x;
-                    l_part[j + 1] += CV::kPaged ? p1 : v1.y + v2.y;
+                    const uint32_t t2 = f32x2_to_e4m3x2((p0 - v1.x) * C::kT2Scale, (p1 - v1.y) * C::kT2Scale);
+                    // the weights before their rounding, so that the lse of a few keys is as exact
+                    // as its scores are
+                    l_part[j] += p0;
+                    l_part[j + 1] += p1;
                     if ((j & 2) == 0) {
                         w1[j / 4] = t1;
                         w2[j / 4] = t2;
@@ -750,7 +780,7 @@ __global__ void __launch_bounds__(192, 1)
                 ++tile_cnt;
             }
             if (!ok) break;
-            // ---------------- epilogue: (O1 + O2) / l -> out (or a partial), lse
+            // ---------------- epilogue: (O1 + 2^-5 O2) / l -> out (or a partial), lse
             ok = ptx::mbar_wait_bounded(pv_done, piece_cnt & 1, tmo);
             if (!ok) break;
             ptx::tc_fence_after();
@@ -798,7 +828,8 @@ __global__ void __launch_bounds__(192, 1)
                     auto store = [&](auto* dst) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            put(dst + at + j * kDv, (__uint_as_float(r1[j]) + __uint_as_float(r2[j])) * fin[c0 + j]);
+                            put(dst + at + j * kDv,
+                                fmaf(__uint_as_float(r2[j]), C::kT2Inv, __uint_as_float(r1[j])) * fin[c0 + j]);
                     };
                     if (pc.slot < 0) store(args.out);
                     else store(args.part_o);
