@@ -354,17 +354,17 @@ mla_status mha_decode_run_phase(const mla_plan* plan, const void* q, const void*
  *   MLA_KERNEL_FP8_PAIR (the default when Sq*H is a multiple of 128): the
  *     codes are the operands of kind::f8f6f4 MMAs on a CTA pair; each q row is
  *     scaled by a power of two and carried as the sum of two E4M3 terms (about
- *     8 significant bits, the precision of a bf16 q), and P (scaled by 2^4) as
- *     the sum of two (about 8 bits, the precision of the bf16 P of the bf16
- *     path).
+ *     8 significant bits, the precision of a bf16 q), and P as the sum of two:
+ *     each weight to about 8 bits (the precision of the bf16 P of the bf16
+ *     path), and what falls below the terms' smallest step, however many keys
+ *     that is, to 2^-7 of a row's weights at most.  lse sums the weights before
+ *     their rounding.
  *   MLA_KERNEL_FP8_MMA (the default otherwise): the codes are the operands of
  *     kind::f8f6f4 tensor-core MMAs as they are; each q row is scaled by a
  *     power of two and carried as the sum of three E4M3 terms (about 12
  *     significant bits, relative error <= 2^-12), and P as the sum of two: each
- *     weight to about 8 bits (the precision of the bf16 P of the bf16 path), and
- *     what falls below the terms' smallest step, however many keys that is, to
- *     2^-7 of a row's weights at most.  lse sums the weights before their
- *     rounding and is as exact as the scores.
+ *     weight to about 8 bits (the precision of the bf16 P of the bf16 path), the
+ *     smaller ones as with MLA_KERNEL_FP8_PAIR; lse too.
  *   MLA_KERNEL_FP8: every E4M3 value divided by 2^8 is exact in f16, so the
  *     kernel widens the codes to those f16 values in shared memory (integer
  *     bit moves) and runs f16 x f16 -> f32 MMAs; q is narrowed from bf16 to f16
@@ -446,8 +446,7 @@ mla_status mla_decode_run_fp8_phase(const mla_plan* plan, const void* q, const v
  *   window        >= 0, 0 = none;  first_tokens  in [0, 2^24], used with a window
  * mha_decode_plan_paged -- as mha_decode_plan, with the same three.
  * mla_decode_plan_paged_fp8 -- the same for pages of E4M3 codes, with the kernels
- * of mla_decode_plan_fp8.  (Both hold lse to the precision of their scores: they
- * sum the weights before their rounding.)
+ * of mla_decode_plan_fp8.
  */
 mla_status mla_decode_plan_paged(int32_t B, int32_t Sq, int32_t H, int32_t L_max, int32_t page_size, int32_t window,
                                  int32_t first_tokens, int32_t device, int32_t num_partitions_override,

@@ -13,15 +13,25 @@
 //      about 8 significant bits (the precision of a bf16 q).  Both terms
 //      multiply the same K chunk into the same S accumulator, so
 //      S = (t1 + t2) K^T and the softmax multiplies each row by 2^-e.
-//   P: carried as 2^4 p, rounded to f16 and written as two E4M3 terms
+//   P: carried as 2^4.75 p, rounded to f16 and written as two E4M3 terms
 //      t1 = e4m3(h), t2 = e4m3(h - t1) (about 8 significant bits, the
 //      precision of the bf16 P of the other kernels); both multiply the same
-//      V chunk into O.  The row sum adds the fp32 weights 2^4 p, so the
-//      factor 2^4 cancels in O / l; the reference max is raised only when a
-//      row max exceeds it by more than 4 (base 2), so 2^4 p <= 256 stays
-//      inside E4M3 while weights down to 2^-10 of the reference keep normal
-//      codes.  (A threshold of 1 with 2^7 p rescaled O several times per
-//      row, each time waiting for the PV in flight.)
+//      V chunk into O, so they have one scale.  The row sum adds the fp32
+//      weights 2^4.75 p, so the factor cancels in O / l; the reference max is
+//      raised when a row max exceeds it by more than 4 (base 2), so
+//      2^4.75 p <= 2^8.75 stays inside E4M3.
+//
+// What the terms lose.  A key's P is off by at most 2^-8 of itself, and by half
+// E4M3's smallest step, 2^-10, where that is more: 2^-3 for a whole tile, where
+// the weight of the reference is 2^4.75.  Thousands of keys below a dominant one
+// that came first can be worth as much as it is and still each be below that
+// step.  So each row adds up what its tiles may have lost, against its sum (both
+// threads of a row know the other's share): past 2^-7 of it, the reference goes
+// down to the tile's maximum (O and the sums are fp32 and scale up).  In all, then, the step
+// loses at most 2^-7 of a row's weights.  On scores of N(0, 2^2) nats references
+// move no more often than when they were only raised; their moves cost less
+// since the exponents' code is there once (64 sequences, 128 heads, L = 8192,
+// such scores: 153 -> 148 us).
 //
 // With K = 32 codes per instruction and two terms, the MMA count and the
 // tensor time per tile are those of the bf16 pair kernel; the cache bytes
@@ -94,9 +104,12 @@ struct PairFp8Cfg {
     // kind::f8f6f4 with E4M3 A and B: format codes 0 (the bit layout of the f16 descriptor)
     static constexpr uint32_t kIdescS = ptx::make_idesc_f16(128, 128, 0, 0);
     static constexpr uint32_t kIdescPV = ptx::make_idesc_f16(128, 256, 0, 1);
-    static constexpr float kLazy = 4.f;        // rescale threshold (base 2): 2^4 p <= 256
-    static constexpr float kPScaleLog2 = 4.f;  // P carried as 2^4 p
-    static constexpr float kPScaleInv = 1.f / 16.f;
+    static constexpr float kLazy = 4.f;           // the reference is raised past this (base 2): P <= 2^8.75 < 448
+    static constexpr float kRaise = 2.f;          // to as much below the row max (fewer moves than to the max itself)
+    static constexpr float kPScaleLog2 = 4.75f;   // P = 2^4.75 p
+    static constexpr float kPScaleInv = 0.0371627223f;
+    static constexpr float kTileLoss = 0x1p-3f;   // the most that the terms' step loses of a tile's P
+    static constexpr float kMaxLoss = 0x1p-7f;    // ... of a piece's weights before the reference goes down
     static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_P % 1024 == 0, "swizzle atoms");
     static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
@@ -705,7 +718,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             }
             const float row_cs = args.scale_log2 * qscale[r];  // score scale of this row (base 2)
             float m_ref = -INFINITY;  // reference max (base 2) of the row, the same in both of its threads
-            float l_part = 0.f;       // this thread's share of the row sum (of 2^4 p), relative to m_ref
+            float l_part = 0.f;       // this thread's share of the row sum (of P), relative to m_ref
+            float lost = 0.f;         // the most that the row's P lost in its terms, relative to m_ref; as m_ref
             SeqView view{};
             RowRange seen{};          // paged: the rows this thread's query row sees
             if constexpr (CV::kPaged) {
@@ -762,13 +776,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 // exps below run
                 const float mloc = ptx::max64(x) * cs;
                 float* redmax = red + (tile_cnt & 1) * 128;
+                float* redl = red + 256 + (tile_cnt & 1) * 128;  // (the epilogue's sums, the piece start's q maxima)
                 redmax[L_id] = mloc;
+                redl[L_id] = l_part;
                 ptx::mbar_arrive(group_sync);
-                // 2^4 P[r][64h .. 64h+63] = exp2(x * cs - m_ref + 4) as two E4M3
+                // P[r][64h .. 64h+63] = exp2(x * cs - m_ref + 4.75) as two E4M3
                 // terms.  Past a piece's first tile the reference max is known
                 // before this tile's max, so P is computed at once; it is redone
-                // only when the row max outgrew the reference by more than 4
-                // (2^4 p <= 256).
+                // only when the reference moves.
                 uint32_t packed[2][16];  // term k: 64 codes in 16 words
                 float lsum = 0.f;
                 auto exps = [&](float m) {
@@ -790,10 +805,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                         // h - first is exact in f16 (a multiple of h's spacing, at most
                         // half the first term's spacing, so under 8 significant bits);
                         // second term = the remainder rounded to E4M3.  The pair holds a
-                        // to about 2^-8 relative (below E4M3's normal range, to its
-                        // subnormal spacing 2^-9: under 2^-13 of the row sum, which
-                        // holds a term of 2^4).  The row sum takes the fp32 weights,
-                        // as in the bf16 kernel.
+                        // to about 2^-8 relative, and to half E4M3's subnormal spacing,
+                        // 2^-10, where that is more (see the reference's moves below).
+                        // The row sum takes the fp32 weights, as in the bf16 kernel.
                         const __half2 h01 = __floats2half2_rn(a[0], a[1]);
                         const __half2 h23 = __floats2half2_rn(a[2], a[3]);
                         const uint32_t c01 = f16x2_to_e4m3x2(h01);
@@ -806,25 +820,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                     }
                     lsum = ls.x + ls.y;
                 };
-                if (!first) exps(m_ref);
-                ok = ptx::mbar_wait_bounded(group_sync, sync_cnt & 1, tmo);
-                ++sync_cnt;
-                if (!ok) break;
-                const float mrow = fmaxf(mloc, redmax[L_id ^ 64]);
                 float alpha = 1.f;
-                bool grow = false;
-                if (first) {
-                    m_ref = CV::kPaged ? fmaxf(mrow, kNoKey) : mrow;
+                bool move = false;  // of a reference of the warp's rows
+                // one copy of the exponents' code, which fills much of the instruction cache
+                bool known = first;  // the row max
+#pragma unroll 1
+                while (true) {
+                    if (known) {
+                        ok = ptx::mbar_wait_bounded(group_sync, sync_cnt & 1, tmo);
+                        ++sync_cnt;
+                        if (!ok) break;
+                        const float mrow = fmaxf(mloc, redmax[L_id ^ 64]);
+                        if (first) {
+                            m_ref = CV::kPaged ? fmaxf(mrow, kNoKey) : mrow;
+                            lost = C::kTileLoss;
+                        } else {
+                            const float total = l_part + redl[L_id ^ 64];
+                            float m = m_ref, w = ex2_approx(mrow - m_ref + C::kPScaleLog2);  // P of the row max
+                            float loss = fminf(C::kTileLoss, kTileKV * w);
+                            if (mrow > m_ref + C::kLazy) m = mrow - C::kRaise;
+                            else if (loss > C::kMaxLoss * w && lost + loss > C::kMaxLoss * (total + w) && total < 0x1p40f)
+                                m = fmaxf(mrow, m_ref - 32.f);
+                            move = __any_sync(0xffffffffu, m > m_ref || m < m_ref);
+                            if (move) {
+                                m = fmaxf(m, mrow - C::kRaise);
+                                alpha = ex2_approx(m_ref - m);
+                                w = ex2_approx(mrow - m + C::kPScaleLog2);
+                                loss = fminf(C::kTileLoss, kTileKV * w);
+                                m_ref = m;
+                                l_part *= alpha;
+                                lost *= alpha;
+                            }
+                            lost += loss;
+                            if (!move) break;
+                        }
+                    }
                     exps(m_ref);
-                } else if (mrow > m_ref + C::kLazy) {
-                    grow = true;
-                    alpha = ex2_approx(m_ref - mrow);
-                    m_ref = mrow;
-                    l_part *= alpha;
-                    exps(m_ref);
+                    if (known) break;
+                    known = true;
                 }
+                if (!ok) break;
                 l_part += lsum;
-                const bool warp_grow = __any_sync(0xffffffffu, grow);
                 const uint32_t pb = (NP == 2) ? (tile_cnt & 1) : 0;
                 // the P buffer is free once the PV that last read it completed
                 // (NP = 1: the previous tile's; NP = 2: the one two tiles back)
@@ -833,7 +869,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                     ok = ptx::mbar_wait_bounded(pv_done + pb, (NP == 2) ? ((v >> 1) & 1) : (v & 1), tmo);
                     if (!ok) break;
                 }
-                if (warp_grow) {
+                if (move) {
                     // O must hold every earlier tile before it is rescaled
                     if (NP == 2) {
                         const uint32_t v = tile_cnt - 1;
@@ -906,7 +942,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
             ok = group_barrier();
             if (!ok) break;
             const int qrow = g * 128 + static_cast<int>(rank) * 64 + r;  // row within the sequence
-            // l and O both carry the factor 2^4 of the P terms
+            // l and O both carry the factor 2^4.75 of the P terms
             float l_row = (l_part + redsum[L_id ^ 64]) * C::kPScaleInv;
             // a sink applies once per row: to whole sequences here, to cut ones in the combine
             float o_fac = 1.f;
