@@ -33,7 +33,7 @@
  *     "host" pointers are ordinary host memory.
  *   - Work is enqueued on `stream` and runs asynchronously; a return of MLA_OK
  *     means the arguments were valid and the launches were accepted.  Faults
- *     detected on the device (timeouts, lengths out of range) are recorded in
+ *     detected on the device (timeouts, lengths or pages out of range) are recorded in
  *     the workspace and reported by mla_decode_check().
  *   - No entry point throws, aborts or prints.
  */
@@ -244,9 +244,10 @@ mla_status mla_decode_run_sinks(const mla_plan* plan, const void* q, const void*
 
 /*
  * mla_decode_check -- synchronize `stream`, read and clear the workspace's
- * device status words.  Returns MLA_OK if no run since the last check
- * recorded a fault, else MLA_ERR_TIMEOUT / MLA_ERR_SEQLEN (the first recorded),
- * or MLA_ERR_CUDA if the synchronization itself failed.
+ * device status words.  Returns MLA_OK if no run (or append with this status
+ * word) since the last check recorded a fault, else the first of MLA_ERR_TIMEOUT,
+ * MLA_ERR_SEQLEN and MLA_ERR_PAGE that was recorded, or MLA_ERR_CUDA if the
+ * synchronization itself failed.
  */
 mla_status mla_decode_check(const mla_plan* plan, void* workspace, void* stream);
 

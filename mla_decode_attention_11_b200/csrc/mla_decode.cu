@@ -304,8 +304,12 @@ const char* mla_status_string(mla_status s) {
         case MLA_ERR_CUDA: return "CUDA call failed";
         case MLA_ERR_TIMEOUT: return "device pipeline wait timed out; results invalid";
         case MLA_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
-        case MLA_ERR_PAGE: return "a block-table entry was outside the cache's pages";
-        case MLA_ERR_SEQLEN: return "a sequence length was outside [0, L_max] (clamped)";
+        case MLA_ERR_SEQLEN:
+            return "a sequence length was outside [0, L_max] (clamped), or an appended token's position outside the "
+                   "rotation table (token skipped)";
+        case MLA_ERR_PAGE:
+            return "a block-table entry was outside the cache's pages (read as zeros), or an appended token's page "
+                   "outside the table or the cache (row not written)";
     }
     return "unknown status";
 }
