@@ -528,8 +528,9 @@ mla_status mla_decode_run_prefix(const mla_plan* plan, const void* q, const void
  * on the way.  The new tokens of all sequences are laid end to end; token i
  * belongs to the sequence b with cu_tokens[b] <= i < cu_tokens[b + 1] and is at
  * position p = seqlens[b] - (cu_tokens[b + 1] - cu_tokens[b]) + i - cu_tokens[b]:
- * seqlens are the lengths with the new tokens, the ones the decode after it is
- * given.  A rotated row x of n columns turns by the angles of p, in fp32:
+ * seqlens are the lengths with the new tokens, the ones the paged decode after it
+ * is given (behind a shared prefix: mla_cache_append_prefix).  A rotated row x of
+ * n columns turns by the angles of p, in fp32:
  *     (x0, x1) -> (x0 c - x1 s, x1 c + x0 s),  c = cos_sin[p][i], s = cos_sin[p][n/2 + i]
  * with the pairs (2i, 2i+1) (interleaved = 1) or (i, i + n/2) (0), and is
  * rounded once, to bf16 or to E4M3.
@@ -575,6 +576,12 @@ typedef struct mla_append {
  * (k, v, q_in and q_out may be NULL then);
  * MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_ALIGNMENT, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA. */
 mla_status mla_cache_append(const mla_append* args, void* stream);
+/* The same for sequences behind a shared prefix: seqlens and block_table are the sequences' own, as
+ * mla_decode_run_prefix takes them.  A token's row goes to its place p among its sequence's own keys; the row and its
+ * queries turn by the angles of prefix_len + p, which is its position behind the prefix (outside [0, num_positions):
+ * skipped and flagged).  prefix_len: device, one int32 >= 0 (else taken as 0 and flagged, MLA_ERR_SEQLEN), the one
+ * that the decode is given; NULL: MLA_ERR_INVALID_ARG.  The prefix itself is appended once, as its own sequence. */
+mla_status mla_cache_append_prefix(const mla_append* args, const int32_t* prefix_len, void* stream);
 /* Enqueue the append of keys and values of grouped kv heads (128 wide, bf16); as mla_cache_append. */
 mla_status mha_cache_append(const mla_append* args, void* stream);
 

@@ -12,7 +12,8 @@ Entry points mirror include/mla_decode.h:
     the paged cache's mla_decode_plan_paged, mla_decode_run_paged,
     mla_decode_plan_paged_fp8, mla_decode_run_paged_fp8,
     mha_decode_plan_paged, mha_decode_run_paged, mla_decode_plan_prefix,
-    mla_decode_run_prefix, mla_cache_append, mha_cache_append
+    mla_decode_run_prefix, mla_cache_append, mla_cache_append_prefix,
+    mha_cache_append
 plus the convenience wrappers ``mla_decode`` (device tensors in, device
 tensors out) and ``mla_decode_host`` (host tensors in and out, with the
 copies done here around the library call).
@@ -53,7 +54,8 @@ EXPORTED_SYMBOLS = ("mla_decode_plan", "mla_decode_plan_kernel", "mla_decode_pla
                     "mla_decode_run_fp8_phase",
                     "mla_decode_plan_paged", "mla_decode_run_paged", "mla_decode_plan_paged_fp8",
                     "mla_decode_run_paged_fp8", "mha_decode_plan_paged", "mha_decode_run_paged",
-                    "mla_decode_plan_prefix", "mla_decode_run_prefix", "mla_cache_append", "mha_cache_append")
+                    "mla_decode_plan_prefix", "mla_decode_run_prefix", "mla_cache_append", "mla_cache_append_prefix",
+                    "mha_cache_append")
 
 
 class MlaError(RuntimeError):
@@ -155,11 +157,12 @@ def load_library(build_if_missing: bool = True):
         lib.mha_decode_run_paged.argtypes = [pp, c_vp, c_vp, c_vp, c_i32] + tail
         lib.mla_decode_run_prefix.argtypes = [pp, c_vp, c_vp, c_i32, c_vp, c_i32, c_vp] + tail
         lib.mla_cache_append.argtypes = [c_vp, c_vp]
+        lib.mla_cache_append_prefix.argtypes = [c_vp, c_vp, c_vp]
         lib.mha_cache_append.argtypes = [c_vp, c_vp]
         for fn in (lib.mla_decode_plan_paged, lib.mha_decode_plan_paged, lib.mla_decode_plan_prefix,
                    lib.mla_decode_plan_paged_fp8, lib.mla_decode_run_paged_fp8, lib.mla_decode_run_paged,
                    lib.mha_decode_run_paged, lib.mla_decode_run_prefix,
-                   lib.mla_cache_append, lib.mha_cache_append):
+                   lib.mla_cache_append, lib.mla_cache_append_prefix, lib.mha_cache_append):
             fn.restype = c_i32
         lib.mla_decode_check.restype = c_i32
         lib.mla_decode_check.argtypes = [ctypes.POINTER(mla_plan), c_vp, c_vp]
@@ -745,7 +748,7 @@ def _query_rows(q_in, q_out, in_name, out_name, T, width, out_width, device):
 
 
 def _append(name, device, T, H, Hkv, k, v, cos_sin, rot, k_pages, v_pages, block_table, seqlens, cu_tokens, q_in, q_out,
-            q_out_offset, strides, kv_scale, interleaved, workspace, stream):
+            q_out_offset, strides, kv_scale, interleaved, workspace, stream, prefix_len=None):
     B = seqlens.shape[0]
     _check_on(seqlens, "seqlens", torch.int32, (B,), device)
     _check_table(block_table, "block_table", B, device)
@@ -753,6 +756,8 @@ def _append(name, device, T, H, Hkv, k, v, cos_sin, rot, k_pages, v_pages, block
     _check_on(cos_sin, "cos_sin", torch.float32, (positions, rot), device)
     if cu_tokens is not None:
         _check_on(cu_tokens, "cu_tokens", torch.int32, (B + 1,), device)
+    if prefix_len is not None:
+        _check_on(prefix_len, "prefix_len", torch.int32, (1,), device)
     if workspace is not None:
         _check_workspace(workspace, device)
         if workspace.data_ptr() == 0 or workspace.nbytes < 256:
@@ -765,7 +770,9 @@ def _append(name, device, T, H, Hkv, k, v, cos_sin, rot, k_pages, v_pages, block
         q_out.data_ptr() + q_out_offset if H else 0, k_pages.data_ptr(),
         v_pages.data_ptr() if v_pages is not None else 0, *strides,
         workspace.data_ptr() if workspace is not None else 0, kv_scale, 0)
-    rc = getattr(_lib or load_library(), name)(args, _stream_on(device, stream))
+    entry = getattr(_lib or load_library(), name)
+    rc = (entry(args, _stream_on(device, stream)) if prefix_len is None else
+          entry(args, prefix_len.data_ptr(), _stream_on(device, stream)))
     if rc != MLA_OK:
         raise MlaError(rc, name)
 
@@ -780,7 +787,8 @@ def mla_cache_append(latent: torch.Tensor, k_rope: torch.Tensor, cos_sin: torch.
                      block_table: torch.Tensor, seqlens: torch.Tensor, cu_tokens: Optional[torch.Tensor] = None,
                      q_rope: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
                      kv_scale: Optional[float] = None, interleaved: bool = True,
-                     workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+                     workspace: Optional[torch.Tensor] = None, stream=None,
+                     prefix_len: Optional[torch.Tensor] = None) -> None:
     """Append T new tokens to a latent cache: latent bf16 [T, 512] and the
     rotated k_rope bf16 [T, 64] become cache rows of kv_pages [pages, page_size,
     576] (bf16, or E4M3 codes of row / kv_scale), and the rotated q_rope bf16
@@ -790,7 +798,11 @@ def mla_cache_append(latent: torch.Tensor, k_rope: torch.Tensor, cos_sin: torch.
     the new tokens; cu_tokens int32 [B + 1]: where each sequence's tokens start
     (None: T / B tokens each).  With a decode workspace, tokens without a
     position or page are reported by mla_decode_check.  A contiguous cache
-    [B, L_max, 576] is a paged one with block_table[b] = [b]."""
+    [B, L_max, 576] is a paged one with block_table[b] = [b].
+
+    Behind a shared prefix (mla_decode_run_prefix), seqlens and block_table are
+    the sequences' own and prefix_len int32 [1] is the decode's: rows and queries
+    then turn by the angles of their positions behind the prefix."""
     device, T = _device_of(latent, "latent"), latent.shape[0]
     k_strides = _rows(latent, "latent", (T, D_V), device)
     v_strides = _rows(k_rope, "k_rope", (T, D_QK - D_V), device)
@@ -801,9 +813,10 @@ def mla_cache_append(latent: torch.Tensor, k_rope: torch.Tensor, cos_sin: torch.
         raise ValueError("kv_scale must be positive and finite in fp32")
     _check_on(kv_pages, "kv_pages", kv_pages.dtype if fp8 else torch.bfloat16, _paged_shape(kv_pages, D_QK), device)
     H, in_strides, out_strides = _query_rows(q_rope, q, "q_rope", "q", T, D_QK - D_V, D_QK, device)
-    _append("mla_cache_append", device, T, H, 1, latent, k_rope, cos_sin, D_QK - D_V, kv_pages, None,
-            block_table, seqlens, cu_tokens, q_rope, q, 2 * D_V, (*k_strides, *v_strides, *in_strides, *out_strides),
-            float(kv_scale) if fp8 else 0.0, interleaved, workspace, stream)
+    _append("mla_cache_append" if prefix_len is None else "mla_cache_append_prefix", device, T, H, 1, latent, k_rope,
+            cos_sin, D_QK - D_V, kv_pages, None, block_table, seqlens, cu_tokens, q_rope, q, 2 * D_V,
+            (*k_strides, *v_strides, *in_strides, *out_strides), float(kv_scale) if fp8 else 0.0, interleaved, workspace,
+            stream, prefix_len)
 
 
 def mha_cache_append(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor, k_pages: torch.Tensor,

@@ -7,9 +7,10 @@
 // row goes to page table[b][p / page_size], row p % page_size; the row's
 // rotated columns, and the token's query rows, turn by the angles of p:
 //     (x0, x1) -> (x0 c - x1 s, x1 c + x0 s),   c, s = cos_sin[p]
-// with pairs (2i, 2i+1) (interleaved) or (i, i + n/2).  All of it is fp32,
-// rounded once when it is written (products and sums each rounded, no fused
-// multiply-add, so the result is the one elementary operations give).
+// with pairs (2i, 2i+1) (interleaved) or (i, i + n/2).  Behind a shared prefix of
+// P keys the row's place is the same and the angles are those of P + p.  All of
+// it is fp32, rounded once when it is written (products and sums each rounded, no
+// fused multiply-add, so the result is the one elementary operations give).
 //
 // Bound by HBM: every input is read once and every output written once, and a
 // token needs only its own rows.  Its work is in tasks of about 2 KB -- its cache
@@ -35,6 +36,7 @@ struct AppendArgs {
     int per_seq;                // tokens of every sequence when cu is null
     const int32_t* cu;          // [B + 1] or null
     const int32_t* seqlens;     // [B], with the new tokens
+    const int32_t* prefix_len;  // keys in front of every sequence, or null
     const int32_t* table;
     long long table_stride;
     int table_width, num_pages, page_size;
@@ -60,14 +62,15 @@ struct AppendArgs {
 constexpr int kAppendThreads = 128;
 constexpr int kAppendRowBytes = 2048;  // head-row bytes of one task
 
-// Sequence and position of token i; position -1: the token is in no sequence
-// (padding) or its position is outside [0, num_positions) (flagged).  Warp-
-// cooperative: each round of the search narrows the bounds 32-fold (the lanes read
+// Sequence and place of token i, and the position whose angles it turns by; place
+// -1: the token is in no sequence (padding), or its place is negative or that
+// position outside [0, num_positions) (flagged).  Warp-cooperative: each round of the search narrows the bounds 32-fold (the lanes read
 // evenly spaced ones, and the last at most i opens the next range), and the last
 // round reads the lengths with them, so that a token's chain of loads is one
 // shorter.
-__device__ __forceinline__ void place_token(const AppendArgs& a, int i, int lane, int& b, int& pos) {
+__device__ __forceinline__ void place_token(const AppendArgs& a, int i, int lane, int& b, int& pos, int& angle) {
     long long next, L;
+    int prefix = a.prefix_len ? __ldg(a.prefix_len) : 0;
     if (a.cu) {
         int lo = 0, n = a.B + 1;  // the answer is in [lo, lo + n)
         while (n > 32) {
@@ -102,8 +105,15 @@ __device__ __forceinline__ void place_token(const AppendArgs& a, int i, int lane
     }
     const long long p = L - next + i;
     pos = -1;
-    if (p >= 0 && p < a.num_positions) pos = static_cast<int>(p);
-    else if (a.status && lane == 0) atomicOr(a.status, kStatusSeqlen);
+    bool good = prefix >= 0;  // (a negative one counts as 0, as in the decode)
+    if (!good) prefix = 0;
+    if (p >= 0 && p + prefix < a.num_positions) {
+        pos = static_cast<int>(p);
+        angle = pos + prefix;
+    } else {
+        good = false;
+    }
+    if (!good && a.status && lane == 0) atomicOr(a.status, kStatusSeqlen);
 }
 
 // Row of the cache for position pos of sequence b, or -1 (flagged).
@@ -266,11 +276,11 @@ __global__ void __launch_bounds__(kAppendThreads) mla_cache_append_kernel(const 
         r1 = *reinterpret_cast<const uint4*>(latent + c1);
         if (lane < 8) raw = *reinterpret_cast<const uint4*>(a.v + i * a.v_token + col);
     }
-    int b, pos;
-    place_token(a, i, lane, b, pos);
+    int b, pos, angle;
+    place_token(a, i, lane, b, pos, angle);
     if (pos < 0) return;
     Angles<kInterleaved> ang;
-    ang.load(a.cos_sin + static_cast<long long>(pos) * a.rot, col, a.rot);
+    ang.load(a.cos_sin + static_cast<long long>(angle) * a.rot, col, a.rot);
     const long long row = row_here ? cache_row(a, b, pos, lane) : -1;
     if (row >= 0) {
         float x[8];
@@ -334,12 +344,12 @@ __global__ void __launch_bounds__(kAppendThreads) mha_cache_append_kernel(const 
     Task at = task_at(t);
     R rows;
     load(rows, at);
-    int b, pos;
-    place_token(a, i, lane, b, pos);
+    int b, pos, angle;
+    place_token(a, i, lane, b, pos, angle);
     if (pos < 0) return;
     const int col = (lane % R::kLanes) * 8;
     Angles<kInterleaved> ang;
-    if (col < a.rot) ang.load(a.cos_sin + static_cast<long long>(pos) * a.rot, col, a.rot);
+    if (col < a.rot) ang.load(a.cos_sin + static_cast<long long>(angle) * a.rot, col, a.rot);
     const long long row = t < 2 * kv_tasks ? cache_row(a, b, pos, lane) : -1;
     while (true) {
         R next;

@@ -614,19 +614,28 @@ mla_status launch_append(void (*kernel)(const mla::AppendArgs), const mla::Appen
     return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
-}  // namespace
-
-extern "C" {
-
-mla_status mla_cache_append(const mla_append* args, void* stream) {
+mla_status mla_append_rows(const mla_append* args, const int32_t* prefix_len, void* stream) {
     mla::AppendArgs a;
     const mla_status st = append_args(args, false, a);
     if (st != MLA_OK) return st;
+    if (!aligned(prefix_len, 4)) return MLA_ERR_ALIGNMENT;
+    a.prefix_len = prefix_len;
     const int per = mla::HeadRows<64>::kHeads, tasks = 1 + (a.H + per - 1) / per;
     const bool fp8 = a.kv_scale > 0.f, il = args->interleaved != 0;
     return launch_append(fp8 ? (il ? mla::mla_cache_append_kernel<true, true> : mla::mla_cache_append_kernel<true, false>)
                              : (il ? mla::mla_cache_append_kernel<false, true> : mla::mla_cache_append_kernel<false, false>),
                          a, tasks, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status mla_cache_append(const mla_append* args, void* stream) { return mla_append_rows(args, nullptr, stream); }
+
+mla_status mla_cache_append_prefix(const mla_append* args, const int32_t* prefix_len, void* stream) {
+    if (!prefix_len) return MLA_ERR_INVALID_ARG;
+    return mla_append_rows(args, prefix_len, stream);
 }
 
 mla_status mha_cache_append(const mla_append* args, void* stream) {
