@@ -559,7 +559,8 @@ typedef struct mla_append {
     const void* v;              /* device bf16: mla: the key's rope part [T, 64]; mha: values [T, Hkv, 128] */
     const void* q_in;           /* device bf16: mla: the queries' rope part [T, H, 64]; mha: queries [T, H, 128] */
     void* q_out;                /* device bf16, same shape: the rotated rows (mla: columns 512.. of a [T, H, 576]
-                                   tensor, whose pointer this is, plus 512).  May be q_in. */
+                                   tensor, whose pointer this is, plus 512).  Its rows must not share memory
+                                   (MLA_ERR_INVALID_ARG).  May be q_in with its strides, else no part of it. */
     void* k_pages;              /* device: mla: the latent cache; mha: the key pages */
     void* v_pages;              /* device: mha: the value pages */
     /* element strides, multiples of 8 (rows are 16-byte aligned, columns contiguous) */

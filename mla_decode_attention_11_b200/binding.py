@@ -742,7 +742,7 @@ def _query_rows(q_in, q_out, in_name, out_name, T, width, out_width, device):
     H = q_in.shape[1] if q_in.dim() == 3 else -1
     in_strides = _rows(q_in, in_name, (T, H, width), device)
     out_strides = _rows(q_out, out_name, (T, H, out_width), device)
-    if (T > 1 and out_strides[0] == 0) or (H > 1 and out_strides[1] == 0):
+    if (T > 1 and out_strides[0] == 0) or (H > 1 and out_strides[1] == 0):  # (others that overlap: the library)
         raise ValueError("the rotated queries' rows must not share memory")
     return H, in_strides, out_strides
 

@@ -538,6 +538,23 @@ mla_status mla_decode_run_prefix(const mla_plan* plan, const void* q, const void
 
 namespace {
 
+// Whether two of T x H rows of `width` elements, at t * token + h * head, share one.
+bool rows_overlap(int64_t T, int64_t token, int64_t H, int64_t head, int64_t width) {
+    token = token < 0 ? -token : token;
+    head = head < 0 ? -head : head;
+    if (T < 2) token = (H - 1) * head + width;
+    if (H < 2) head = (T - 1) * token + width;
+    if (head >= width && token >= (H - 1) * head + width) return false;
+    if (token >= width && head >= (T - 1) * token + width) return false;
+    // neither lies in the other's gaps as a block: the row nearest to h heads on, for every h
+    if (token < width || head < width) return true;
+    for (int64_t h = 1; h < H; ++h) {
+        const int64_t t = std::min(h * head / token, T - 1), rest = h * head - t * token;
+        if (rest < width || (t + 1 < T && token - rest < width)) return true;
+    }
+    return false;
+}
+
 // Checks what both kinds of append share and fills the kernel's arguments.
 mla_status append_args(const mla_append* p, bool mha, mla::AppendArgs& a) {
     if (!p || !p->seqlens || !p->block_table || !p->cos_sin || !p->k_pages) return MLA_ERR_INVALID_ARG;
@@ -559,6 +576,9 @@ mla_status append_args(const mla_append* p, bool mha, mla::AppendArgs& a) {
                                p->q_in_token_stride, p->q_in_head_stride, p->q_out_token_stride, p->q_out_head_stride};
     for (int64_t s : strides)
         if (s % 8 != 0) return MLA_ERR_ALIGNMENT;
+    if (p->T > 0 && p->H > 0 &&
+        rows_overlap(p->T, p->q_out_token_stride, p->H, p->q_out_head_stride, mha ? 128 : 64))
+        return MLA_ERR_INVALID_ARG;
     std::memset(&a, 0, sizeof a);
     a.B = p->B;
     a.T = p->T;

@@ -3,6 +3,7 @@ arguments whose memory a call would corrupt or misread are refused before anythi
 import ctypes
 
 import pytest
+import torch
 
 from mla_decode_attention_11_b200 import binding as M
 from tests.test_paged_boundary import FIELDS
@@ -39,3 +40,24 @@ def test_append_behind_a_prefix_rejects(lib):
     assert call(16, B=0) == 1 and call(16, cos_sin=8) == 2
     assert call(16, T=0, k=0, v=0) == 0  # nothing to do
     assert lib.mla_cache_append_prefix(None, ctypes.c_void_p(16), None) == 1
+
+
+@pytest.mark.parametrize("T,H,token,head,overlap", [
+    (4, 4, 0, 64, True), (4, 4, 256, 0, True), (4, 4, 64, 8, True), (4, 4, 248, 64, True), (4, 4, 64, 248, True),
+    (2, 3, 128, 64, True), (3, 2, 64, 128, True), (4, 4, -256, 56, True), (5, 3, 104, 312, True),
+    (4, 4, 256, 64, False), (4, 4, 64, 256, False), (4, 4, -256, 64, False), (1, 4, 0, 64, False), (4, 1, 64, 0, False),
+    (1, 1, 0, 0, False), (2, 3, 64, 128, False), (3, 2, 128, 64, False), (2, 2, 72, 1000, False)])
+@pytest.mark.parametrize("scale", [1, 2])
+def test_rotated_queries_that_share_memory_are_refused(lib, scale, T, H, token, head, overlap):
+    """Rows of the rotated queries that overlap would be written by several warps at once.  (Latent rows turn 64 columns,
+    others hold 128.  A call whose strides pass goes on to the device, and fails here for want of one.)"""
+    rows = [range(t * token + h * head, t * token + h * head + 64) for t in range(T) for h in range(H)]
+    touched = [e for r in rows for e in r]
+    assert (len(set(touched)) < len(touched)) == overlap  # the case is what it says
+    if not overlap and torch.cuda.is_available():
+        pytest.skip("the made-up pointers would reach a device")
+    fn, width = ((lib.mla_cache_append, 64), (lib.mha_cache_append, 128))[scale - 1]
+    kw = dict(B=1, T=T, H=H, cu_tokens=0, q_in=16, q_out=16, q_in_token_stride=width * H, q_in_head_stride=width,
+              q_out_token_stride=token * scale, q_out_head_stride=head * scale, v_token_stride=width)
+    got = fn(packed(**kw), None)
+    assert got == 1 if overlap else got not in (0, 1, 2)
