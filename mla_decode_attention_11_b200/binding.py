@@ -713,6 +713,7 @@ def rope_table(num_positions: int, dim: int, base: float = 10000.0, device=None)
     return torch.cat([angle.cos(), angle.sin()], dim=1).float()
 
 
+_FLT_MAX = torch.finfo(torch.float32).max
 _APPEND = struct.Struct("=10iq10Q8qQfi")  # the fields of mla_append, in order
 
 
@@ -809,7 +810,7 @@ def mla_cache_append(latent: torch.Tensor, k_rope: torch.Tensor, cos_sin: torch.
     fp8 = kv_pages.dtype in (torch.uint8, torch.float8_e4m3fn)
     if fp8 != (kv_scale is not None):
         raise ValueError("kv_scale goes with a cache of E4M3 codes (torch.uint8 or torch.float8_e4m3fn)")
-    if fp8 and not 2.0 ** -149 <= kv_scale < 2.0 ** 127:  # 0 in fp32 would ask for bf16 rows
+    if fp8 and not 2.0 ** -149 <= kv_scale <= _FLT_MAX:  # 0 in fp32 would ask for bf16 rows
         raise ValueError("kv_scale must be positive and finite in fp32")
     _check_on(kv_pages, "kv_pages", kv_pages.dtype if fp8 else torch.bfloat16, _paged_shape(kv_pages, D_QK), device)
     H, in_strides, out_strides = _query_rows(q_rope, q, "q_rope", "q", T, D_QK - D_V, D_QK, device)

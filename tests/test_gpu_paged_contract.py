@@ -1,6 +1,8 @@
 """GPU tests of what the paged calls promise one another and their callers: an append behind a shared prefix turns by the
 positions that the prefix's decode means, faults are told apart, arguments that would corrupt memory are refused.
 Tolerances as in test_gpu_paged."""
+import math
+
 import pytest
 import torch
 
@@ -122,3 +124,20 @@ def test_append_behind_a_prefix_flags(cuda_device):
     for bad, error in ((ints([0, 0]), ValueError), (ints([0]).long(), TypeError), (ints([0]).cpu(), ValueError)):
         with pytest.raises(error):
             M.mla_cache_append(row[:, :512], row[:, 512:], cos_sin, kv, table, sl, prefix_len=bad)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -149, 2.0 ** 126, 2.0 ** 127, 3e38, torch.finfo(torch.float32).max])
+def test_append_takes_every_scale_of_fp32(cuda_device, scale):
+    """Scales up to fp32's largest are positive and finite there; the codes are those of a division in 32 bits."""
+    x = torch.arange(0, 65536, 16, device=DEV).to(torch.int32).to(torch.int16).view(torch.bfloat16).view(8, 512)
+    x = torch.where(torch.isnan(x), 0.0, x)
+    kv = torch.zeros(1, 16, 576, dtype=torch.uint8, device=DEV)
+    table, sl = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.tensor([8], dtype=torch.int32, device=DEV)
+    call = lambda s: M.mla_cache_append(x, torch.zeros(8, 64, dtype=torch.bfloat16, device=DEV),
+                                        M.rope_table(8, 64, device=DEV), kv, table, sl, kv_scale=s)
+    call(scale)
+    want = (x.float() / torch.tensor(scale, device=DEV)).clamp(-448, 448).to(torch.float8_e4m3fn).float()
+    assert torch.equal(kv[0, :8, :512].contiguous().view(torch.float8_e4m3fn).float(), want)
+    for bad in (2.0 ** 128, 3.5e38, math.inf):
+        with pytest.raises(ValueError):
+            call(bad)
