@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from mla_decode_attention_11_b200 import binding as M
-from tests.test_gpu_paged import DEV, LONG, Pages, blank, close, rand, reference, seen_mask, turn_tolerance, turned
+from tests.test_gpu_paged import (DEV, LONG, Pages, blank, close, make_prefix, make_window, rand, reference, seen_mask,
+                                  turn_tolerance, turned)
 
 pytestmark = pytest.mark.gpu
 
@@ -141,3 +142,68 @@ def test_append_takes_every_scale_of_fp32(cuda_device, scale):
     for bad in (2.0 ** 128, 3.5e38, math.inf):
         with pytest.raises(ValueError):
             call(bad)
+
+
+@pytest.mark.parametrize("kind,H,Hkv", [("mla", 16, 1), ("mla", 128, 1), ("mla_fp8", 32, 1), ("mla_fp8", 128, 1),
+                                        ("mha", 8, 2)])
+def test_lengths_out_of_range_are_reported_as_such(cuda_device, kind, H, Hkv):
+    """A length past L_max or below zero is clamped and reported as MLA_ERR_SEQLEN: where every table entry is good nothing
+    else could be, and where pages are bad as well it comes first."""
+    page, L_max, B = 64, 256, 3
+    lengths = [100, 256, 30]
+    run, _, (out, lse), (plan, ws, pages, sl, q) = make_window(kind, lengths, 1, H, Hkv, page, 0, 0, False, 19, L_max=L_max)
+    # good pages everywhere: those of the second sequence, which is full
+    pages.table.copy_(pages.table[1].expand(B, -1).clone())
+    for bad, taken in ((L_max + 1, L_max), (2 ** 31 - 1, L_max), (-1, 0), (-2 ** 31, 0)):
+        sl[0] = taken
+        want = blank(*out.shape[:3], out.shape[3])
+        run(*want)
+        M.mla_decode_check(plan, ws)
+        sl[0] = bad
+        out.fill_(float("nan"))
+        run(out, lse)
+        with pytest.raises(M.MlaError) as e:
+            M.mla_decode_check(plan, ws)
+        assert e.value.code == 7, bad
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        M.mla_decode_check(plan, ws)  # reported once
+    sl[0], pages.table[2, 0] = L_max + 1, -1
+    run(out, lse)
+    with pytest.raises(M.MlaError) as e:
+        M.mla_decode_check(plan, ws)
+    assert e.value.code == 7
+    sl[0] = 100
+    run(out, lse)
+    with pytest.raises(M.MlaError) as e:
+        M.mla_decode_check(plan, ws)
+    assert e.value.code == 8
+
+
+@pytest.mark.parametrize("most", [512, LONG])
+@pytest.mark.parametrize("H", [16, 128])
+def test_prefix_lengths_out_of_range_are_reported_as_such(cuda_device, H, most):
+    """The same for the prefix's length, in both forms, and for the lengths behind a prefix."""
+    run, _, (out, lse), (plan, ws, pages, sl, pl) = make_prefix([30, 0, 200], 1, H, 512, 64, False, seed=6, prefix_max=most,
+                                                                L_max=256)
+    # one good page for every entry of every table
+    pages.k.nan_to_num_(0.5)
+    pages.table.fill_(1)
+    table = torch.ones(most // 64, dtype=torch.int32, device=DEV)
+    B, scale = 3, 576 ** -0.5
+
+    def call(o, l):
+        M.mla_decode_run_prefix(plan, run.q, pages.k, table, pl, pages.table[:B], sl, scale, o, l, ws)
+    for what, bad, taken in ((pl, most + 1, most), (pl, -5, 0), (sl[1:2], 257, 256), (sl[1:2], -1, 0)):
+        keep = int(what)
+        what.fill_(taken)
+        want = blank(*out.shape[:3], 512)
+        call(*want)
+        M.mla_decode_check(plan, ws)
+        what.fill_(bad)
+        out.fill_(float("nan"))
+        call(out, lse)
+        with pytest.raises(M.MlaError) as e:
+            M.mla_decode_check(plan, ws)
+        assert e.value.code == 7, bad
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        what.fill_(keep)
