@@ -22,16 +22,17 @@
 //      max exceeds it by more than 4 (base 2), so 2^4 p <= 256 stays inside
 //      E4M3 (and 2^5 times its remainder, at most 8).
 //
-// What the terms lose.  A key's 2^4 p is off by at most 2^-8 of itself, and by
-// 2^-14 where t1 has no normal code (below 2^-6): in p, 128 * 2^-18 = 2^-11 of
-// 2^m for a whole tile.  Thousands of keys below a dominant one that came first
-// can be worth as much as it is and still each be below that step.  So for each
-// query row a lane of every warp weighs the tiles, each by its maximum: at one
-// far below the reference, where 2^-11 a tile so far is more than 2^-7 of that
-// weight, the reference goes down to the tile's maximum (O and the sums are fp32
-// and scale up).  In all, then, the step loses at most 2^-7 of a row's weights.
-// On scores of N(0, 2^2) nats this moves references hardly more often than raising
-// them alone; counting only tiles, without their weights, cost 10 %.
+// What the terms lose.  A key's 2^4 p is off by at most 2^-8 of itself (and 2^-11,
+// since the terms are taken of it rounded to f16), and by 2^-14 where t1 has no
+// normal code (below 2^-6): in p, 128 * 2^-18 = 2^-11 of 2^m for a whole tile.
+// Thousands of keys below a dominant one that came first can be worth as much as
+// it is and still each be below that step.  So for each query row a lane of every
+// warp weighs the tiles, each by its maximum: at one far below the reference,
+// where 2^-11 a tile so far is more than 2^-7 of that weight, the reference goes
+// down to the tile's maximum (O and the sums are fp32 and scale up).  In all, then,
+// the step loses at most 2^-7 of a row's weights.  On scores of N(0, 2^2) nats
+// this moves references hardly more often than raising them alone; counting only
+// tiles, without their weights, cost 10 % there.
 //
 // K and V are exact; the errors are the truncation of q (<= 2^-12 relative)
 // and of p (as above), and fp32 accumulation.  A host-side emulation
@@ -135,6 +136,19 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
 __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t codes) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xFFFFu), __NV_E4M3);
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// An f16 pair -> two E4M3 codes (round to nearest even, saturating at +-448);
+// the low byte holds the low half.
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(__half2 h) {
+    return static_cast<uint32_t>(
+        __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&h), __NV_SATFINITE, __NV_E4M3));
+}
+
+// The two values of an E4M3 code pair as an f16 pair, exactly.
+__device__ __forceinline__ __half2 e4m3x2_to_f16x2(uint32_t codes) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xFFFFu), __NV_E4M3);
+    return *reinterpret_cast<const __half2*>(&h);
 }
 
 // The largest e with amax * 2^e <= 448 (0 for amax = 0), kept in [-120, 120].
@@ -739,9 +753,12 @@ __global__ void __launch_bounds__(192, 1)
                 for (int j = 0; j < G; j += 2) {
                     const float p0 = ex2_approx(x[j] - m_ref[j] + C::kPScaleLog2);
                     const float p1 = ex2_approx(x[j + 1] - m_ref[j + 1] + C::kPScaleLog2);
-                    const uint32_t t1 = f32x2_to_e4m3x2(p0, p1);
-                    const float2 v1 = e4m3x2_to_f32x2(t1);
-                    const uint32_t t2 = f32x2_to_e4m3x2((p0 - v1.x) * C::kT2Scale, (p1 - v1.y) * C::kT2Scale);
+                    // through f16 pairs (2^-11 of the weight; the remainder h - t1 is exact): in fp32
+                    // the terms took 3 more instructions a pair, 2 to 6 % of a decode
+                    const __half2 h = __floats2half2_rn(p0, p1);
+                    const uint32_t t1 = f16x2_to_e4m3x2(h);
+                    const __half2 rest = __hmul2(__hsub2(h, e4m3x2_to_f16x2(t1)), __float2half2_rn(C::kT2Scale));
+                    const uint32_t t2 = f16x2_to_e4m3x2(rest);
                     // the weights before their rounding, so that the lse of a few keys is as exact
                     // as its scores are
                     l_part[j] += p0;

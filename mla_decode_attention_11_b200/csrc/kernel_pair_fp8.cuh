@@ -57,19 +57,6 @@
 
 namespace mla {
 
-// An f16 pair -> two E4M3 codes (round to nearest even, saturating at +-448);
-// the low byte holds the low half.
-__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(__half2 h) {
-    return static_cast<uint32_t>(
-        __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&h), __NV_SATFINITE, __NV_E4M3));
-}
-
-// The two values of an E4M3 code pair as an f16 pair, exactly.
-__device__ __forceinline__ __half2 e4m3x2_to_f16x2(uint32_t codes) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xFFFFu), __NV_E4M3);
-    return *reinterpret_cast<const __half2*>(&h);
-}
-
 template <int NK, int NV, int NS, int NP, bool kPaged = false>
 struct PairFp8Cfg {
     static constexpr int kThreads = 256;

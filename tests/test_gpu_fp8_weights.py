@@ -6,7 +6,7 @@ A score is one product: the query is zero but in a rope column (not a value colu
 times the head's query element, exactly, and a head's element sets how far the scores spread.  The 64-bit definition is
 computed from the same codes.
 
-Tolerances.  P is carried as two E4M3 terms: a weight is off by at most 2^-8 of itself (and 2^-11 where it passes through
+Tolerances.  P is carried as two E4M3 terms: a weight is off by at most 2^-8 of itself (and 2^-11, as it passes through
 f16), and by the terms' smallest step, whose sum over a sequence's keys the kernels hold below 2^-7 of the weights' sum.
 The sums that normalise are of the weights themselves.  With A = sum p |v| / sum p and V = max |v|, out is off by
 (2^-8 + 2^-11) A + 2^-7 V, and by 2^-8 of itself from its rounding.  Scores are fp32 products of exact factors: 2^-22 of
