@@ -59,7 +59,8 @@ PrefixLayout prefix_layout(const mla_plan& pl) {
 // With fewer, a sequence's own pass over the prefix takes NG / 148 of its tiles'
 // time each, about 2.7 us a tile of a CTA, and the second launch and the partials
 // some 20 us: the two are level at 8 tiles a CTA (64 sequences, 16 heads: 41 and
-// 41 us; at 4 29 and 39, at 16 64 and 45).
+// 41 us; at 4 29 and 39, at 16 64 and 45).  The plan decides, by the longest prefix
+// that it allows: a short one behind a plan for long ones takes the two launches.
 bool prefix_in_front(const mla_plan& pl) {
     if (pl.kernel == MLA_KERNEL_PAIR) return true;
     const int64_t tiles = (static_cast<int64_t>(pl.prefix_max) + mla::kTileKV - 1) / mla::kTileKV;
@@ -618,7 +619,7 @@ mla_status append_args(const mla_append* p, bool mha, mla::AppendArgs& a) {
 
 // A token's tasks go to so many warps that there are about 8 an SM in all: 2178
 // tokens of 6 tasks, kv in L2, take 10.6 us so (2 tasks a warp: 11.8, one: 13.2).
-constexpr int64_t kAppendWarps = 148 * 8;
+constexpr int64_t kAppendWarpsPerSm = 8;
 
 mla_status launch_append(void (*kernel)(const mla::AppendArgs), const mla::AppendArgs& a, int tasks,
                          cudaStream_t stream) {
@@ -627,8 +628,14 @@ mla_status launch_append(void (*kernel)(const mla::AppendArgs), const mla::Appen
     any.device = -1;
     const mla_status st = check_run_device(any);
     if (st != MLA_OK) return st;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return MLA_ERR_CUDA;
+    }
     const int64_t per = mla::kAppendThreads / 32;
-    const int64_t parts = std::min<int64_t>(tasks, (kAppendWarps + a.T - 1) / a.T);
+    const int64_t parts = std::min<int64_t>(tasks, (kAppendWarpsPerSm * sms + a.T - 1) / a.T);
     const dim3 grid(static_cast<unsigned>((a.T + per - 1) / per), static_cast<unsigned>(parts));
     kernel<<<grid, mla::kAppendThreads, 0, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
