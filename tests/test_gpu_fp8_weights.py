@@ -106,3 +106,53 @@ def test_weights_of_all_sizes(cuda_device, paged, H, parts, name):
         tol = delta + 2.0 ** -20 * (1 + l.abs())
         err = (lse[b, 0].double() - l).abs()
         assert (err <= tol).all(), f"L {L}: lse off by {err.max().item():.2e}, {(err / tol).max().item():.2f} tolerances"
+
+
+@pytest.mark.parametrize("name", ["first", "first_noisy", "falling", "tails"])
+@pytest.mark.parametrize("parts", [1, 7])
+@pytest.mark.parametrize("H,Sq", [(16, 1), (16, 2), (64, 2), (128, 2)])
+def test_first_tokens_and_a_window(cuda_device, H, Sq, parts, name):
+    """The dominant key among the first tokens that stay visible, the others in a window of 9000: tiles of the first
+    tokens, none in between, the window's; two query tokens see ranges one apart; sinks weigh too."""
+    g = torch.Generator().manual_seed(12)
+    page, ks, window, first = 16, 1.0 / 64, 9000, 4
+    L_max = -(-N // page) * page
+    lengths = [N, 8192, 1, 300]
+    B = len(lengths)
+    codes = torch.zeros(B, L_max, 576)
+    codes[..., :512] = torch.randint(32, 97, (B, L_max, 512), generator=g).float()
+    codes[:, :first, :512] = -64.0
+    for b, L in enumerate(lengths):
+        codes[b, :L, 540] = profile(name, L, g) * 64
+    codes = codes.to(torch.float8_e4m3fn)
+    spread = (6 + 8 * torch.arange(H) / H).mul(16).round().div(16)
+    q = torch.zeros(B, Sq, H, 576, dtype=torch.bfloat16)
+    q[..., 540] = spread
+    sinks = torch.linspace(-3, 9, H)
+    q, codes, sinks = q.to(DEV), codes.to(DEV), sinks.to(DEV)
+    sl = torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    out = torch.full((B, Sq, H, 512), float("nan"), dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((B, Sq, H), float("nan"), dtype=torch.float32, device=DEV)
+    plan = M.mla_decode_plan_paged_fp8(B, Sq, H, L_max, page, window=window, first_tokens=first, device=0,
+                                       num_partitions=parts)
+    ws = M.alloc_workspace(plan)
+    table = torch.arange(B * L_max // page, dtype=torch.int32, device=DEV).view(B, -1)
+    M.mla_decode_run_paged_fp8(plan, q, codes.view(-1, page, 576), ks, table, sl, 1.0, out, lse, ws, sinks=sinks)
+    M.mla_decode_check(plan, ws)
+    for b, L in enumerate(lengths):
+        kv = codes[b, :L].double() * ks
+        for t in range(Sq):
+            p = L - Sq + t
+            j = torch.arange(L, device=DEV)
+            seen = (j <= p) & ((j > p - window) | (j < first))
+            s = torch.where(seen, spread.to(DEV).double()[:, None] * kv[:, 540], -math.inf)
+            l = torch.logaddexp(torch.logsumexp(s, 1), sinks.double())
+            w = torch.exp(s - l[:, None])
+            o, a = w @ kv[:, :512], w @ kv[:, :512].abs()
+            delta = 2.0 ** -22 * torch.where(seen, s.abs(), 0.0).amax(1)
+            lost = 2.0 ** -7 * kv[:, :512].abs().max() * w.sum(1)[:, None]
+            tol = (2.0 ** -8 + 2.0 ** -11 + 2 * delta[:, None] + 2.0 ** -20) * a + lost + 2.0 ** -8 * o.abs()
+            err = (out[b, t].double() - o).abs()
+            assert (err <= tol).all(), f"L {L} token {t}: out off by {err.max().item():.4f}"
+            tol = delta + 2.0 ** -20 * (1 + l.abs())
+            assert ((lse[b, t].double() - l).abs() <= tol).all(), f"L {L} token {t}: lse"
